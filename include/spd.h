@@ -362,6 +362,114 @@ int spd_grouped_gemv(const void* const* W, const float* const* x, float* const* 
                      int32_t rows, int32_t cols, int32_t dtype, const float* nw, float eps,
                      void* cuda_stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * The attention block of a decode step for many continuations of one prompt: 4-bit projections,
+ * rotary positions with the cache append, attention of a batch that shares a prefix.  Device
+ * pointers of the current device unless marked HOST, enqueued on `cuda_stream`; no call keeps state
+ * between calls, allocates or synchronises, and all of them can be captured into a graph.
+ * ------------------------------------------------------------------------------------------- */
+
+/* Rotary positions.  Pair i (0 <= i < rot_dim/2) of a head turns by pos * f_i:
+ *   (a, b) -> mscale * (a cos - b sin, a sin + b cos);
+ * the pair is elements (i, i + rot_dim/2) in the half layout, (2i, 2i + 1) in the interleaved one;
+ * elements from rot_dim on are copied.  f_i = theta^(-2i/rot_dim), scaled for contexts `factor` times
+ * the original one:
+ *   SPD_ROPE_LINEAR  f_i / factor (position interpolation)
+ *   SPD_ROPE_NTK     theta * factor^(r/(r-2)) in the place of theta, r = rot_dim (r = 2: no change)
+ *   SPD_ROPE_YARN    f_i / factor * (1 - g_i) + f_i * g_i, g_i = 1 - clamp((i - lo)/(hi - lo), 0, 1),
+ *                    lo = floor(D(32)), hi = ceil(D(1)), both clamped to 0..r/2-1 (hi - lo to >= 0.001),
+ *                    D(b) = r ln(original_context / (2 pi b)) / (2 ln theta); mscale = 0.1 ln(factor) + 1
+ * (mscale is 1 elsewhere).  The plan is plain host data: fill it once, pass it by pointer (HOST).
+ * SPD_EINVAL: head_dim not a multiple of 16 in 16..256, rot_dim not even in 2..head_dim, theta <= 1,
+ * factor < 1 (scaled kinds), original_context < 1 (YaRN). */
+#define SPD_ROPE_MAX_PAIRS 128
+enum { SPD_ROPE_HALF = 0, SPD_ROPE_INTERLEAVED = 1 };
+enum { SPD_ROPE_NONE = 0, SPD_ROPE_LINEAR = 1, SPD_ROPE_NTK = 2, SPD_ROPE_YARN = 3 };
+typedef struct spd_rope {
+  int32_t head_dim, rot_dim, layout;
+  float mscale;
+  uint64_t turns[SPD_ROPE_MAX_PAIRS]; /* f_i / 2 pi in units of 2^-64 */
+} spd_rope;
+int spd_rope_init(spd_rope* out, int32_t head_dim, int32_t rot_dim, int32_t layout, double theta,
+                  int32_t scaling, double factor, int32_t original_context);
+
+/* Rotate the queries and keys of T tokens and append the keys and values to a cache.
+ *   q [T][n_heads][hd], k, v [T][n_kv_heads][hd] in x_dtype, token t starting at t * stride elements
+ *   (so that the three may be parts of one fused projection row); q_out like q, and may be q itself.
+ *   pos [T]: position index of each token (any int32; a negative one turns backwards).
+ *   k_cache, v_cache [n_seqs][n_kv_heads][max_seq][hd] in cache_dtype; token t goes to row slot[t] of
+ *   sequence seq[t] (seq NULL: sequence 0).  A token whose slot lies outside 0..max_seq-1 or whose
+ *   sequence lies outside 0..n_seqs-1 is rotated but not appended (padding); other rows of the cache
+ *   are left as they were.  No two tokens of a call may name the same row.
+ * n_heads or n_kv_heads may be 0 (their pointers are ignored); T = 0 does nothing.  Angles are exact
+ * at any position (64-bit fixed point), products are fp32.  Any alignment of the elements' own size
+ * works; 16-byte aligned rows (and rot_dim / 2 a multiple of 16 bytes in the half layout) are faster. */
+int spd_rope_append(const spd_rope* rope, const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                    const void* k, int64_t k_stride, const void* v, int64_t v_stride, int32_t x_dtype,
+                    const int32_t* pos, int32_t T, int32_t n_heads, int32_t n_kv_heads, void* k_cache,
+                    void* v_cache, int32_t cache_dtype, const int32_t* slot, const int32_t* seq,
+                    int32_t n_seqs, int32_t max_seq, void* cuda_stream);
+
+/* 4-bit weights with group scales: W[r][c] = (code[r][c] - zero[r][c / group]) * scale[r][c / group].
+ *   codes  uint8 [rows][cols/2], even column in the low nibble;
+ *   scales [rows][cols/group] in scale_dtype;  zeros uint8 [rows][cols/group], or NULL: all 8.
+ * group 32, 64 or 128; cols a multiple of group, at most 32768; rows >= 1.
+ *
+ * spd_q4_quantize makes them from a matrix [rows][cols] in `dtype`, rounding to nearest (ties to
+ * even).  Without zeros scale = max|w| / 7; with zeros scale = (max(w, 0) - min(w, 0)) / 15 and
+ * zero = round(-min(w, 0) / scale).  The scale is rounded to scale_dtype before it is used; a group
+ * of scale 0 gets code = zero.  Weights must be finite.
+ *
+ * spd_q4_pack lays the three arrays out for spd_q4_gemv, once, into `packed` (16-byte aligned,
+ * spd_q4_packed_bytes): for each 16 rows and 128 columns one record of codes, scales and zeros, in the
+ * order in which a warp multiplies them. */
+size_t spd_q4_packed_bytes(int32_t rows, int32_t cols, int32_t group, int32_t scale_dtype, int32_t has_zeros);
+int spd_q4_quantize(const void* w, int32_t dtype, int32_t rows, int32_t cols, int32_t group, int32_t scale_dtype,
+                    uint8_t* codes, void* scales, uint8_t* zeros, void* cuda_stream);
+int spd_q4_pack(const uint8_t* codes, const void* scales, const uint8_t* zeros, int32_t rows, int32_t cols,
+                int32_t group, int32_t scale_dtype, void* packed, size_t packed_bytes, void* cuda_stream);
+
+/* Grouped matrix-vector products with packed 4-bit weights: for each group g (HOST array of G, 1..34)
+ *   y_g[m][r] = sum_c W_g[r][c] * x_g[m][c],  m < M (1..32),
+ * x_g optionally RMS-normalised: x / rms(x) * nw (nw fp32 [cols] shared by all groups, or NULL).
+ * x [M] rows of cols elements and y [M] rows of `rows` elements, both in x_dtype, row m starting at
+ * m * stride.  All groups share cols, group, scale_dtype and has_zeros.  fp32 vectors are multiplied
+ * exactly (three bf16 terms each), bf16 vectors as they are (normalised ones as two bf16 terms);
+ * sums are fp32 in an order fixed by the sizes.  Groups must not write the same y.  SPD_EINVAL on bad
+ * sizes, NULL pointers, or unaligned ones (packed weights 16 bytes, x, y and nw their element). */
+typedef struct spd_q4_group {
+  const void* w;     /* spd_q4_pack's output */
+  const void* x;
+  void* y;
+  int64_t x_stride, y_stride; /* elements between vectors */
+  int32_t rows;
+  int32_t reserved;  /* 0 */
+} spd_q4_group;
+int spd_q4_gemv(const spd_q4_group* groups, int32_t G, int32_t M, int32_t cols, int32_t group, int32_t scale_dtype,
+                int32_t has_zeros, int32_t x_dtype, const float* nw, float eps, void* cuda_stream);
+
+/* Decode attention of B sequences that share a prefix: sequence b's query sees the prefix keys
+ * 0..prefix_len-1 and its own keys 0..lens[b]-1,
+ *   out[b][h][:] = softmax(q[b][h] . K^T / sqrt(hd)) V,   lse[b][h] = log sum exp(q[b][h] . K^T / sqrt(hd)).
+ * The prefix is read once for the whole batch.
+ *   q, out [B][n_heads][hd] in q_dtype (fp32 queries keep fp32 accuracy, bf16 ones bf16's);
+ *   prefix_k, prefix_v bf16 [n_kv_heads][prefix_cap][hd]; k_cache, v_cache bf16 [B][n_kv_heads][max_seq][hd];
+ *   lens int32 [B], read on the device (a captured call follows them); lse fp32 [B][n_heads] or NULL.
+ * hd 64 or 128; n_heads at most 1024; B 0..4096 (0: nothing to do); 0 <= prefix_len <= prefix_cap (0: the prefix pointers may be NULL); max_seq >= 0
+ * (0: no sequence has keys of its own, the cache pointers and lens may be NULL).  Rows of the caches from
+ * prefix_len or lens[b] on are not used, whatever they hold.  A sequence without any key gets out = 0 and
+ * lse = -inf; one whose lens[b] lies outside 0..max_seq gets NaN.  Every pointer 16-byte aligned (lens
+ * and lse 4).  `workspace` (>= spd_shared_prefix_attention_workspace_bytes, 16-byte aligned) holds
+ * partial results of this call only: it needs no initialisation, and calls that may overlap on the GPU
+ * need one each. */
+size_t spd_shared_prefix_attention_workspace_bytes(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                                   int32_t prefix_len);
+int spd_shared_prefix_attention(const void* q, int32_t q_dtype, const void* prefix_k, const void* prefix_v,
+                                int32_t prefix_len, int32_t prefix_cap, const void* k_cache, const void* v_cache,
+                                const int32_t* lens, int32_t max_seq, int32_t B, int32_t n_heads, int32_t n_kv_heads,
+                                int32_t head_dim, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

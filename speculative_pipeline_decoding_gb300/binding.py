@@ -71,6 +71,21 @@ class spd_cycle_info(ctypes.Structure):
                  "pdm_top2", "draft_token", "pushed_token")]
 
 
+ROPE_MAX_PAIRS = 128
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+class spd_rope(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("mscale", ctypes.c_float), ("turns", ctypes.c_uint64 * ROPE_MAX_PAIRS)]
+
+
+class spd_q4_group(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64), ("rows", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class spd_stats(ctypes.Structure):
     _fields_ = [("cycles", ctypes.c_int64), ("exits", ctypes.c_int64), ("rejects", ctypes.c_int64),
                 ("committed", ctypes.c_int64), ("device_ms", ctypes.c_double),
@@ -95,7 +110,7 @@ def lib() -> ctypes.CDLL:
         raise SpdError(-3, f"SPD CUDA library missing at {path}; build it with "
                            "speculative_pipeline_decoding_gb300.build_ext.build()")
     L = ctypes.CDLL(path)
-    vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     sig = {
         "spd_create": (ctypes.c_int, [ctypes.POINTER(spd_config), ctypes.POINTER(spd_weights), vp,
                                       ctypes.POINTER(vp)]),
@@ -127,6 +142,16 @@ def lib() -> ctypes.CDLL:
                                                         vp, vp]),
         "spd_prefill_attention_workspace_bytes": (sz, [i32, i32, i32, i32]),
         "spd_prefill_attention": (ctypes.c_int, [vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, sz, vp]),
+        "spd_rope_init": (ctypes.c_int, [vp, i32, i32, i32, ctypes.c_double, i32, ctypes.c_double, i32]),
+        "spd_rope_append": (ctypes.c_int, [vp, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp, i32, i32, i32, vp, vp, i32,
+                                           vp, vp, i32, i32, vp]),
+        "spd_q4_packed_bytes": (sz, [i32, i32, i32, i32, i32]),
+        "spd_q4_quantize": (ctypes.c_int, [vp, i32, i32, i32, i32, i32, vp, vp, vp, vp]),
+        "spd_q4_pack": (ctypes.c_int, [vp, vp, vp, i32, i32, i32, i32, vp, sz, vp]),
+        "spd_q4_gemv": (ctypes.c_int, [vp, i32, i32, i32, i32, i32, i32, i32, vp, ctypes.c_float, vp]),
+        "spd_shared_prefix_attention_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
+        "spd_shared_prefix_attention": (ctypes.c_int, [vp, i32, vp, vp, i32, i32, vp, vp, vp, i32, i32, i32, i32, i32, vp,
+                                                       vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -448,3 +473,269 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     _check(lib().spd_prefill_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), int(pos0), R, hq, hkv, hd, max_seq,
                                        _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                        _stream_handle(stream)))
+
+
+# ---------------------------------------------------------------------------
+# the attention block of a decode step for many continuations of one prompt
+# ---------------------------------------------------------------------------
+_DT = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+
+
+def _bad(msg: str) -> "SpdError":
+    return SpdError(-1, msg)
+
+
+def _call(fn, args, device: int, stream) -> None:
+    """Runs a C entry on the tensors' device, on `stream` or else torch's current stream there."""
+    if stream is not None:
+        s = _stream_handle(stream)
+    elif _raw_stream is not None:
+        s = _raw_stream(device)
+    else:
+        s = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device:
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, s)
+    if rc:
+        _check(rc)
+
+
+def _device(ts) -> int:
+    """Ordinal of the one GPU that all of `ts` live on."""
+    d = -1
+    for t in ts:
+        if t is None:
+            continue
+        i = t.get_device()
+        if i < 0:
+            raise _bad("tensor must live on the GPU")
+        if d < 0:
+            d = i
+        elif i != d:
+            raise _bad("tensors live on different GPUs")
+    return d
+
+
+def _heads(name: str, t: torch.Tensor, hd: int) -> int:
+    """Token stride of a [T, heads, hd] tensor whose tokens are contiguous."""
+    if t.dim() != 3 or t.size(2) != hd:
+        raise _bad(f"{name} must be [T, heads, {hd}]")
+    if t.size(0) and t.size(1) and (t.stride(2) != 1 or (t.size(1) > 1 and t.stride(1) != hd)):
+        raise _bad(f"{name}: the heads of a token must be contiguous")
+    # the stride of a dimension of size 1 says nothing
+    return t.stride(0) if t.size(0) > 1 else t.size(1) * hd
+
+
+def _ints(name: str, t: torch.Tensor, n: int) -> int:
+    if t.dtype != torch.int32 or t.dim() != 1 or t.size(0) != n or not t.is_contiguous():
+        raise _bad(f"{name} must be a contiguous int32 tensor of {n} elements")
+    return t.data_ptr()
+
+
+class Rope:
+    """Rotary positions: the frequencies of ``rot_dim / 2`` pairs of a head, made once on the host.
+
+    ``layout`` "half" pairs elements (i, i + rot_dim/2), "interleaved" (2i, 2i + 1).  ``scaling`` "linear", "ntk" or
+    "yarn" stretches the context by ``factor`` (YaRN: from ``original_context`` positions)."""
+
+    def __init__(self, head_dim: int, rot_dim: Optional[int] = None, layout: str = "half", theta: float = 10000.0,
+                 scaling: str = "none", factor: float = 1.0, original_context: int = 0):
+        if layout not in ROPE_LAYOUTS:
+            raise _bad(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
+        if scaling not in ROPE_SCALINGS:
+            raise _bad(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+        self.c = spd_rope()
+        self.head_dim = int(head_dim)
+        self.rot_dim = self.head_dim if rot_dim is None else int(rot_dim)
+        _check(lib().spd_rope_init(ctypes.addressof(self.c), self.head_dim, self.rot_dim, ROPE_LAYOUTS[layout], float(theta),
+                                   ROPE_SCALINGS[scaling], float(factor), int(original_context)))
+        self._at = ctypes.addressof(self.c)
+
+
+def rope_append(rope: Rope, q: Optional[torch.Tensor], q_out: Optional[torch.Tensor], pos: torch.Tensor, k=None, v=None,
+                k_cache=None, v_cache=None, slot=None, seq=None, stream=None) -> None:
+    """Rotate q [T, Hq, hd] into q_out (which may be q) and append the rotated k and v [T, Hkv, hd] to the caches.
+
+    pos int32 [T]: position indices.  Caches [n_seqs, Hkv, max_seq, hd] or, for one sequence, [Hkv, max_seq, hd]; token t
+    goes to row slot[t] of sequence seq[t] (0 without seq); a slot or sequence out of range is padding: not appended.
+    q, k, v share a dtype (fp32 or bf16) and may be parts of one fused row (any token stride); the caches are fp32 or
+    bf16.  Without k only q is rotated; q may be None with k given.  ``stream``: None is torch's current stream."""
+    hd = rope.head_dim
+    dev = _device((q, q_out, pos, k, v, k_cache, v_cache, slot, seq))
+    T = pos.numel()
+    qp = qo = kp = vp = kcp = vcp = sp = sqp = None
+    qs = qos = ks = vs = hq = hkv = n_seqs = max_seq = 0
+    x = q if q is not None else k
+    if x is None:
+        raise _bad("q and k are both None")
+    if x.dtype not in _DT:
+        raise _bad("q, k and v must be fp32 or bf16")
+    cdt = x.dtype
+    if q is not None:
+        if q_out is None or q_out.shape != q.shape or q_out.dtype != q.dtype or q.size(0) != T:
+            raise _bad("q_out must have q's shape and dtype, and pos one entry a token")
+        qs, qos, hq, qp, qo = _heads("q", q, hd), _heads("q_out", q_out, hd), q.size(1), q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise _bad("q_out without q")
+    if k is not None:
+        if v is None or k_cache is None or v_cache is None or slot is None:
+            raise _bad("k needs v, k_cache, v_cache and slot")
+        if k.dtype != x.dtype or v.dtype != x.dtype or v.shape != k.shape or k.size(0) != T:
+            raise _bad("k and v must have q's dtype and tokens, and one shape")
+        ks, vs, hkv, kp, vp = _heads("k", k, hd), _heads("v", v, hd), k.size(1), k.data_ptr(), v.data_ptr()
+        shape = k_cache.shape
+        cdt = k_cache.dtype
+        if (len(shape) not in (3, 4) or shape[-3] != hkv or shape[-1] != hd or v_cache.shape != shape or v_cache.dtype != cdt
+                or cdt not in _DT or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+            raise _bad("caches must be contiguous [n_seqs, Hkv, max_seq, hd] or [Hkv, max_seq, hd] in fp32 or bf16")
+        n_seqs, max_seq = (shape[0] if len(shape) == 4 else 1), shape[-2]
+        kcp, vcp, sp = k_cache.data_ptr(), v_cache.data_ptr(), _ints("slot", slot, T)
+        if seq is not None:
+            sqp = _ints("seq", seq, T)
+    elif v is not None or k_cache is not None or v_cache is not None or slot is not None or seq is not None:
+        raise _bad("v, the caches, slot and seq belong to k")
+    _call(lib().spd_rope_append, (rope._at, qp, qs, qo, qos, kp, ks, vp, vs, _DT[x.dtype], _ints("pos", pos, T), T, hq, hkv,
+                                  kcp, vcp, _DT[cdt], sp, sqp, n_seqs, max_seq), dev, stream)
+
+
+class Q4Matrix:
+    """A [rows, cols] matrix of 4-bit codes with group scales, laid out for :func:`q4_gemv` (see :func:`q4_pack`)."""
+
+    def __init__(self, packed: torch.Tensor, rows: int, cols: int, group: int, scale_dtype: torch.dtype, has_zeros: bool):
+        self.packed, self.rows, self.cols, self.group = packed, rows, cols, group
+        self.scale_dtype, self.has_zeros = scale_dtype, has_zeros
+        self._kind = (cols, group, _DT[scale_dtype], int(has_zeros))
+        self._ptr, self._dev = packed.data_ptr(), packed.get_device()
+
+
+def q4_quantize(w: torch.Tensor, group: int = 128, symmetric: bool = True, scale_dtype: torch.dtype = torch.bfloat16, stream=None):
+    """4-bit codes uint8 [rows, cols/2] (even column in the low nibble), scales [rows, cols/group] and, when not symmetric,
+    zero points uint8 [rows, cols/group] (else None) of a matrix in fp32 or bf16, rounded to nearest."""
+    if w.dim() != 2 or w.dtype not in _DT or not w.is_contiguous() or scale_dtype not in _DT:
+        raise _bad("w must be a contiguous fp32 or bf16 matrix, scale_dtype fp32 or bf16")
+    rows, cols = w.shape
+    dev = _device((w,))
+    if group not in (32, 64, 128) or cols % group:
+        raise _bad("group must be 32, 64 or 128 and divide the columns")
+    codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=w.device)
+    scales = torch.empty(rows, cols // group, dtype=scale_dtype, device=w.device)
+    zeros = None if symmetric else torch.empty(rows, cols // group, dtype=torch.uint8, device=w.device)
+    _call(lib().spd_q4_quantize, (w.data_ptr(), _DT[w.dtype], rows, cols, group, _DT[scale_dtype], codes.data_ptr(),
+                                  scales.data_ptr(), None if zeros is None else zeros.data_ptr()), dev, stream)
+    return codes, scales, zeros
+
+
+def q4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor] = None, stream=None) -> Q4Matrix:
+    """Lays codes, scales and zero points (as :func:`q4_quantize` gives them) out for :func:`q4_gemv`, once."""
+    if (codes.dim() != 2 or codes.dtype != torch.uint8 or scales.dim() != 2 or scales.dtype not in _DT
+            or scales.size(0) != codes.size(0) or scales.size(1) < 1 or not codes.is_contiguous() or not scales.is_contiguous()):
+        raise _bad("codes must be contiguous uint8 [rows, cols/2], scales fp32 or bf16 [rows, cols/group]")
+    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape or not zeros.is_contiguous()):
+        raise _bad("zeros must be contiguous uint8 in the scales' shape")
+    dev = _device((codes, scales, zeros))
+    rows, cols = codes.size(0), codes.size(1) * 2
+    group = cols // scales.size(1)
+    if group not in (32, 64, 128) or group * scales.size(1) != cols:
+        raise _bad("the scales must come in groups of 32, 64 or 128 columns")
+    n = lib().spd_q4_packed_bytes(rows, cols, group, _DT[scales.dtype], int(zeros is not None))
+    if n == 0:
+        raise _bad("matrix sizes out of range")
+    packed = torch.empty(n, dtype=torch.uint8, device=codes.device)
+    _call(lib().spd_q4_pack, (codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(), rows, cols, group,
+                              _DT[scales.dtype], packed.data_ptr(), n), dev, stream)
+    return Q4Matrix(packed, rows, cols, group, scales.dtype, zeros is not None)
+
+
+def q4_gemv(Ws: Sequence[Q4Matrix], xs: Sequence[torch.Tensor], ys: Sequence[torch.Tensor],
+            norm_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None) -> None:
+    """ys[g][m] = Ws[g] @ (rmsnorm(xs[g][m]) * norm_weight if norm_weight is given else xs[g][m]) for up to 32 vectors m.
+
+    xs [M, cols] and ys [M, rows], or one vector [cols] and [rows]; fp32 or bf16, all in one dtype; rows contiguous, any
+    row stride.  The matrices share columns, group, scale dtype and the presence of zero points."""
+    G = len(Ws)
+    if G < 1 or G > 34 or len(xs) != G or len(ys) != G:
+        raise _bad("q4_gemv takes 1 to 34 matrices, with a vector and an output each")
+    kind, dev, x0 = Ws[0]._kind, Ws[0]._dev, xs[0]
+    cols, dt, nd = kind[0], x0.dtype, x0.dim()
+    M = 1 if nd == 1 else x0.size(0)
+    if dt not in _DT or nd not in (1, 2):
+        raise _bad("xs must be fp32 or bf16, [M, cols] or [cols]")
+    arr = (spd_q4_group * G)()
+    for g in range(G):
+        W, x, y = Ws[g], xs[g], ys[g]
+        if W._kind != kind:
+            raise _bad("the matrices of a call share columns, group, scale dtype and zero points")
+        if (x.dtype != dt or y.dtype != dt or x.dim() != nd or y.dim() != nd or x.size(-1) != cols or y.size(-1) != W.rows
+                or x.stride(-1) != 1 or (y.stride(-1) != 1 and W.rows > 1)):
+            raise _bad(f"group {g}: x must be [M, {cols}] and y [M, {W.rows}], one dtype, contiguous rows")
+        if nd == 2 and (x.size(0) != M or y.size(0) != M):
+            raise _bad("all groups take the same number of vectors")
+        if x.get_device() != dev or y.get_device() != dev or W._dev != dev:
+            raise _bad("tensors must live on one GPU")
+        a = arr[g]
+        a.w, a.x, a.y, a.rows = W._ptr, x.data_ptr(), y.data_ptr(), W.rows
+        if M > 1:
+            a.x_stride, a.y_stride = x.stride(0), y.stride(0)
+    nw = None
+    if norm_weight is not None:
+        if (norm_weight.dtype != torch.float32 or norm_weight.dim() != 1 or norm_weight.numel() != cols or not norm_weight.is_contiguous()
+                or norm_weight.get_device() != dev):
+            raise _bad(f"norm_weight must be a contiguous fp32 vector of {cols} elements on the same GPU")
+        nw = norm_weight.data_ptr()
+    if M == 0:
+        return
+    _call(lib().spd_q4_gemv, (ctypes.addressof(arr), G, M, cols, kind[1], kind[2], kind[3], _DT[dt], nw, eps), dev, stream)
+
+
+def shared_prefix_attention_workspace_bytes(B: int, n_heads: int, n_kv_heads: int, head_dim: int, prefix_len: int) -> int:
+    """Workspace of a call, or 0 for sizes that it refuses."""
+    return int(lib().spd_shared_prefix_attention_workspace_bytes(B, n_heads, n_kv_heads, head_dim, prefix_len))
+
+
+def shared_prefix_attention(q: torch.Tensor, prefix_k: Optional[torch.Tensor], prefix_v: Optional[torch.Tensor], prefix_len: int,
+                            k_cache: Optional[torch.Tensor], v_cache: Optional[torch.Tensor], lens: Optional[torch.Tensor],
+                            out: torch.Tensor, workspace: torch.Tensor, lse: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Attention of one query per sequence over a shared prefix and the sequence's own keys.
+
+    q, out [B, Hq, hd] (fp32 or bf16); prefix_k, prefix_v [Hkv, prefix_cap, hd] bf16, of which the first prefix_len rows
+    count; k_cache, v_cache [B, Hkv, max_seq, hd] bf16 with lens int32 [B] rows each (None: no own keys); lse fp32 [B, Hq]
+    or None.  A sequence without keys gets 0 and lse -inf, one with lens out of range NaN."""
+    if q.dim() != 3 or q.dtype not in _DT or out.shape != q.shape or out.dtype != q.dtype:
+        raise _bad("q and out must be [B, Hq, hd] in fp32 or bf16")
+    if not q.is_contiguous() or not out.is_contiguous() or not workspace.is_contiguous():
+        raise _bad("q, out and the workspace must be contiguous")
+    dev = _device((q, prefix_k, prefix_v, k_cache, v_cache, lens, out, workspace, lse))
+    B, hq, hd = q.shape
+    hkv = 0
+    pkp = pvp = kcp = vcp = lp = ep = None
+    cap = max_seq = 0
+    if prefix_k is not None:
+        if (prefix_v is None or prefix_k.dim() != 3 or prefix_k.dtype != torch.bfloat16 or prefix_k.size(2) != hd
+                or prefix_v.shape != prefix_k.shape or prefix_v.dtype != torch.bfloat16 or not prefix_k.is_contiguous()
+                or not prefix_v.is_contiguous()):
+            raise _bad(f"prefix_k and prefix_v must be contiguous bf16 [Hkv, prefix_cap, {hd}]")
+        hkv, cap, pkp, pvp = prefix_k.size(0), prefix_k.size(1), prefix_k.data_ptr(), prefix_v.data_ptr()
+    elif prefix_v is not None:
+        raise _bad("prefix_v without prefix_k")
+    if k_cache is not None:
+        if (v_cache is None or lens is None or k_cache.dim() != 4 or k_cache.dtype != torch.bfloat16 or k_cache.size(0) != B
+                or k_cache.size(3) != hd or v_cache.shape != k_cache.shape or v_cache.dtype != torch.bfloat16
+                or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+            raise _bad(f"k_cache and v_cache must be contiguous bf16 [{B}, Hkv, max_seq, {hd}], with lens")
+        if hkv and k_cache.size(1) != hkv:
+            raise _bad("the prefix and the caches differ in kv heads")
+        hkv, max_seq, kcp, vcp, lp = k_cache.size(1), k_cache.size(2), k_cache.data_ptr(), v_cache.data_ptr(), _ints("lens", lens, B)
+    elif v_cache is not None or lens is not None:
+        raise _bad("v_cache and lens belong to k_cache")
+    if not hkv:
+        raise _bad("neither a prefix nor caches")
+    if lse is not None:
+        if lse.dtype != torch.float32 or lse.shape != (B, hq) or not lse.is_contiguous():
+            raise _bad("lse must be a contiguous fp32 [B, Hq]")
+        ep = lse.data_ptr()
+    _call(lib().spd_shared_prefix_attention, (q.data_ptr(), _DT[q.dtype], pkp, pvp, prefix_len, cap, kcp, vcp, lp, max_seq, B, hq, hkv,
+                                              hd, out.data_ptr(), ep, workspace.data_ptr(),
+                                              workspace.numel() * workspace.element_size()), dev, stream)

@@ -1,0 +1,177 @@
+"""Argument checks of the decode-block operators, on the host: every refusal returns before any CUDA call."""
+import ctypes
+import math
+
+import pytest
+
+FAKE = 1 << 20  # an aligned address that no refused call touches
+
+
+@pytest.fixture(scope="module")
+def L():
+    from speculative_pipeline_decoding_gb300 import build_ext, binding
+    build_ext.build()
+    return binding.lib()
+
+
+def _message(L):
+    return L.spd_last_error(None).decode()
+
+
+def _rope(**kw):
+    a = dict(hd=128, rot=128, layout=0, theta=1e4, scaling=0, factor=1.0, context=0)
+    a.update(kw)
+    return tuple(a.values())
+
+
+@pytest.mark.parametrize("bad", [dict(hd=24, rot=16), dict(hd=0), dict(hd=272, rot=16), dict(rot=0), dict(rot=3), dict(rot=130), dict(layout=2),
+                                 dict(layout=-1), dict(theta=1.0), dict(theta=math.nan), dict(theta=math.inf), dict(scaling=4),
+                                 dict(scaling=-1), dict(scaling=1, factor=0.5), dict(scaling=2, factor=math.nan),
+                                 dict(scaling=1, factor=math.inf), dict(scaling=3, factor=2.0)])
+def test_rope_init_refuses(L, bad):
+    from speculative_pipeline_decoding_gb300.binding import spd_rope
+    r = spd_rope()
+    assert L.spd_rope_init(ctypes.addressof(r), *_rope(**bad)) == -1
+    assert "spd_rope_init" in _message(L)
+    assert L.spd_rope_init(None, *_rope()) == -1
+
+
+@pytest.mark.parametrize("scaling,factor,context,theta,rot", [("none", 1.0, 0, 1e4, 128), ("linear", 4.0, 0, 1e4, 64), ("ntk", 8.0, 0, 1e4, 96),
+                                                              ("yarn", 8.0, 32768, 1e4, 128), ("yarn", 4.0, 7, 1.01, 10), ("none", 1.0, 0, 1e4, 2)])
+def test_rope_plan_holds_the_frequencies(L, scaling, factor, context, theta, rot):
+    """Turns in units of 2^-64, against the formulas in Python's doubles (2^-52 relative: both round a power)."""
+    from speculative_pipeline_decoding_gb300.binding import Rope
+    r = Rope(128, rot, theta=theta, scaling=scaling, factor=factor, original_context=context)
+    base = theta * factor ** (rot / (rot - 2)) if scaling == "ntk" else theta
+    top = rot // 2 - 1
+    lo = hi = 0
+    if scaling == "yarn":
+        d = lambda b: rot * math.log(context / (2 * math.pi * b)) / (2 * math.log(base))  # noqa: E731
+        lo, hi = min(max(math.floor(d(32)), 0), top), min(max(math.ceil(d(1)), 0), top)
+    for i in range(rot // 2):
+        f = base ** (-2 * i / rot)
+        if scaling == "linear":
+            f /= factor
+        if scaling == "yarn":
+            g = 1 - min(max((i - lo) / max(hi - lo, 0.001), 0), 1)
+            f = f / factor * (1 - g) + f * g
+        assert r.c.turns[i] / 2.0 ** 64 == pytest.approx(f / (2 * math.pi), rel=1e-13)
+    assert r.c.mscale == pytest.approx(0.1 * math.log(factor) + 1 if scaling == "yarn" else 1.0, rel=1e-6)
+
+
+def test_rope_names_are_checked(L):
+    from speculative_pipeline_decoding_gb300.binding import Rope, SpdError
+    for kw in (dict(layout="rows"), dict(scaling="cubic"), dict(rot_dim=5)):
+        with pytest.raises(SpdError):
+            Rope(128, **kw)
+
+
+def _append(L, plan, **kw):
+    a = dict(q=FAKE, qs=1024, qo=FAKE, qos=1024, k=FAKE, ks=256, v=FAKE, vs=256, xdt=0, pos=FAKE, T=2, hq=8, hkv=2, kc=FAKE, vc=FAKE, cdt=1,
+             slot=FAKE, seq=None, n_seqs=1, max_seq=4)
+    a.update(kw)
+    return L.spd_rope_append(plan, *a.values(), None)
+
+
+@pytest.mark.parametrize("bad", [dict(q=None), dict(qo=None), dict(pos=None), dict(k=None), dict(v=None), dict(kc=None), dict(vc=None),
+                                 dict(slot=None), dict(qs=1023), dict(qos=1000), dict(ks=255), dict(vs=0), dict(qos=2048), dict(xdt=2),
+                                 dict(cdt=-1), dict(T=-1), dict(hq=-1), dict(hq=0, hkv=0), dict(hkv=-2), dict(n_seqs=0), dict(max_seq=0)])
+def test_rope_append_refuses(L, bad):
+    from speculative_pipeline_decoding_gb300.binding import Rope
+    assert _append(L, Rope(128)._at, **bad) == -1
+    assert "spd_rope_append" in _message(L)
+
+
+def test_rope_append_refuses_foreign_plans_and_takes_no_tokens(L):
+    from speculative_pipeline_decoding_gb300.binding import Rope, spd_rope
+    assert _append(L, None) == -1
+    assert _append(L, ctypes.addressof(spd_rope())) == -1
+    assert _append(L, Rope(128)._at, T=0) == 0
+
+
+def test_q4_sizes(L):
+    n = L.spd_q4_packed_bytes
+    assert n(16, 128, 128, 1, 0) == 1024 + 32
+    assert n(17, 160, 32, 0, 1) == 2 * 2 * (1024 + 4 * 64 + 4 * 32)
+    for bad in ((0, 128, 128, 1, 0), (16, 96, 128, 1, 0), (16, 192, 128, 1, 0), (16, 128, 16, 1, 0), (16, 32768 + 128, 128, 1, 0),
+                (16, 128, 128, 2, 0), (16, 0, 32, 1, 0), (-1, 128, 128, 1, 0)):
+        assert n(*bad) == 0
+
+
+def test_q4_quantize_and_pack_refuse(L):
+    z, p = L.spd_q4_quantize, L.spd_q4_pack
+    for bad in ((None, 0, 4, 128, 128, 1, FAKE, FAKE, None), (FAKE, 2, 4, 128, 128, 1, FAKE, FAKE, None), (FAKE, 0, 4, 128, 128, 1, None, FAKE, None),
+                (FAKE, 0, 4, 128, 128, 1, FAKE, None, None), (FAKE + 2, 0, 4, 128, 128, 1, FAKE, FAKE, None), (FAKE, 1, 4, 128, 128, 0, FAKE, FAKE + 2, None),
+                (FAKE, 0, 0, 128, 128, 1, FAKE, FAKE, None), (FAKE, 0, 4, 100, 128, 1, FAKE, FAKE, None)):
+        assert z(*bad, None) == -1 and "spd_q4_quantize" in _message(L)
+    for bad in ((None, FAKE, None, 16, 128, 128, 1, FAKE, 1 << 20), (FAKE, None, None, 16, 128, 128, 1, FAKE, 1 << 20), (FAKE, FAKE, None, 16, 128, 128, 1, None, 1 << 20),
+                (FAKE, FAKE, None, 16, 128, 128, 1, FAKE + 8, 1 << 20), (FAKE, FAKE, None, 16, 128, 128, 1, FAKE, 1055),
+                (FAKE, FAKE, FAKE, 16, 128, 128, 1, FAKE, 1056), (FAKE, FAKE + 1, None, 16, 128, 128, 1, FAKE, 1 << 20), (FAKE, FAKE, None, 16, 128, 64, 3, FAKE, 1 << 20)):
+        assert p(*bad, None) == -1 and "spd_q4_pack" in _message(L)
+
+
+def _gemv(L, groups=1, group=None, **kw):
+    from speculative_pipeline_decoding_gb300.binding import spd_q4_group
+    g = dict(w=FAKE, x=FAKE, y=FAKE, x_stride=256, y_stride=64, rows=64, reserved=0)
+    g.update(group or {})
+    arr = (spd_q4_group * max(1, groups))(*[spd_q4_group(**g) for _ in range(max(1, groups))])
+    a = dict(G=groups, M=2, cols=256, group=128, sdt=1, z=0, xdt=0, nw=None, eps=1e-6)
+    a.update(kw)
+    return L.spd_q4_gemv(ctypes.addressof(arr), *a.values(), None)
+
+
+@pytest.mark.parametrize("bad", [dict(groups=0), dict(groups=35), dict(M=0), dict(M=33), dict(cols=100), dict(cols=0), dict(cols=65536),
+                                 dict(group=dict(w=None)), dict(group=dict(x=None)), dict(group=dict(y=None)), dict(group=dict(rows=0)),
+                                 dict(group=dict(w=FAKE + 8)), dict(group=dict(x=FAKE + 2)), dict(group=dict(y=FAKE + 1)), dict(group=dict(x_stride=255)),
+                                 dict(group=dict(y_stride=63)), dict(sdt=2), dict(xdt=3), dict(nw=FAKE + 2), dict(nw=FAKE, eps=-1.0),
+                                 dict(nw=FAKE, eps=math.nan)])
+def test_q4_gemv_refuses(L, bad):
+    assert _gemv(L, **bad) == -1
+    assert "spd_q4_gemv" in _message(L)
+
+
+def test_q4_gemv_refuses_other_group_sizes(L):
+    from speculative_pipeline_decoding_gb300.binding import spd_q4_group
+    arr = (spd_q4_group * 1)(spd_q4_group(FAKE, FAKE, FAKE, 256, 64, 64, 0))
+    for n in (0, 16, 48, 256):
+        assert L.spd_q4_gemv(ctypes.addressof(arr), 1, 1, 256, n, 1, 0, 0, None, 1e-6, None) == -1
+    assert L.spd_q4_gemv(None, 1, 1, 256, 128, 1, 0, 0, None, 1e-6, None) == -1
+
+
+def _attn(L, **kw):
+    a = dict(q=FAKE, dt=1, pk=FAKE, pv=FAKE, P=100, cap=128, kc=FAKE, vc=FAKE, lens=FAKE, max_seq=16, B=4, hq=8, hkv=2, hd=128, out=FAKE, lse=FAKE,
+             ws=FAKE, wsb=1 << 40)
+    a.update(kw)
+    return L.spd_shared_prefix_attention(*a.values(), None)
+
+
+@pytest.mark.parametrize("bad", [dict(q=None), dict(dt=2), dict(pk=None), dict(pv=None), dict(P=-1), dict(P=129), dict(kc=None), dict(vc=None),
+                                 dict(lens=None), dict(max_seq=-1), dict(B=-1), dict(B=4097), dict(hq=7), dict(hkv=0), dict(hd=96), dict(hd=256),
+                                 dict(out=None), dict(ws=None), dict(wsb=0), dict(q=FAKE + 8), dict(pk=FAKE + 2), dict(pv=FAKE + 4), dict(kc=FAKE + 2),
+                                 dict(vc=FAKE + 2), dict(out=FAKE + 2), dict(lens=FAKE + 2), dict(lse=FAKE + 1), dict(ws=FAKE + 4), dict(hq=2048)])
+def test_shared_prefix_attention_refuses(L, bad):
+    assert _attn(L, **bad) == -1
+    assert "spd_shared_prefix_attention" in _message(L)
+
+
+def test_shared_prefix_attention_empty_batch_and_workspace(L):
+    assert _attn(L, B=0) == 0
+    n = L.spd_shared_prefix_attention_workspace_bytes
+    assert n(4, 8, 2, 128, 1000) > 0 and n(1, 8, 8, 64, 0) > 0
+    for bad in ((0, 8, 2, 128, 10), (4, 7, 2, 128, 10), (4, 8, 2, 96, 10), (4, 8, 2, 128, -1), (4097, 8, 2, 128, 10)):
+        assert n(*bad) == 0
+
+
+def test_binding_refuses_tensors_off_the_gpu(L):
+    import torch
+    import speculative_pipeline_decoding_gb300 as spd
+    q, pos = torch.zeros(2, 8, 128), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(spd.SpdError):
+        spd.rope_append(spd.Rope(128), q, q, pos)
+    with pytest.raises(spd.SpdError):
+        spd.q4_quantize(torch.zeros(16, 128))
+    with pytest.raises(spd.SpdError):
+        spd.q4_pack(torch.zeros(16, 64, dtype=torch.uint8), torch.zeros(16, 1))
+    kv = torch.zeros(2, 4, 128, dtype=torch.bfloat16)
+    with pytest.raises(spd.SpdError):
+        spd.shared_prefix_attention(q, kv, kv, 4, None, None, None, q.clone(), torch.zeros(1 << 16, dtype=torch.uint8))

@@ -1,0 +1,562 @@
+"""The attention block of a decode step for many continuations (4-bit products, rotary positions with the cache append,
+shared-prefix attention) against plain formulas in 64 bits.
+
+Tolerances count roundings: half a step of a stored value (2^-24 of it in fp32, 2^-8 in bf16), and one step of fp32
+(2^-23) of the sum of magnitudes for each addition of a chain of tensor-core or fp32 sums."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+HALF = {F32: 2.0 ** -24, BF16: 2.0 ** -8}
+U = 2.0 ** -23
+
+
+@pytest.fixture(scope="module")
+def spd():
+    from speculative_pipeline_decoding_gb300 import build_ext
+    build_ext.build()
+    import speculative_pipeline_decoding_gb300 as spd
+    return spd
+
+
+def _g(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _rn(g, *shape, dtype=F32, std=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)
+
+
+def _close(got, want, tol):
+    """Element by element; `want` and `tol` in 64 bits."""
+    got = got.double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    err = (got - want).abs()
+    bad = ~(err <= tol) & ~torch.isnan(want) & ~(got == want)
+    n = int(bad.sum())
+    assert n == 0, (n, float((err / tol.clamp(min=1e-300))[bad].max()))
+
+
+# ---------------------------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------------------------
+def _freqs(rot, theta=10000.0, scaling="none", factor=1.0, context=0):
+    r = rot
+    if scaling == "ntk" and r > 2:
+        theta = theta * factor ** (r / (r - 2))
+    f = torch.tensor([theta ** (-2 * i / r) for i in range(r // 2)], dtype=torch.float64)
+    if scaling == "linear":
+        f = f / factor
+    m = 1.0
+    if scaling == "yarn":
+        top = r // 2 - 1
+        d = lambda b: r * math.log(context / (2 * math.pi * b)) / (2 * math.log(theta))  # noqa: E731
+        lo, hi = min(max(math.floor(d(32)), 0), top), min(max(math.ceil(d(1)), 0), top)
+        g = 1 - ((torch.arange(r // 2, dtype=torch.float64) - lo) / max(hi - lo, 0.001)).clamp(0, 1)
+        f = f / factor * (1 - g) + f * g
+        m = 0.1 * math.log(factor) + 1
+    return f.cuda(), m
+
+
+def _rot64(x, pos, f, m, rot, layout):
+    """(rotated x, magnitude of each element's pair) in 64 bits."""
+    x = x.double()
+    y, mag = x.clone(), x.abs()
+    ang = pos.double()[:, None, None] * f
+    c, s = ang.cos() * m, ang.sin() * m
+    i = (slice(0, rot // 2), slice(rot // 2, rot)) if layout == "half" else (slice(0, rot, 2), slice(1, rot, 2))
+    a, b = x[..., i[0]], x[..., i[1]]
+    y[..., i[0]], y[..., i[1]] = a * c - b * s, a * s + b * c
+    mag[..., i[0]] = mag[..., i[1]] = (a.abs() + b.abs()) * m
+    return y, mag
+
+
+# The angle's float holds half a turn in 24 bits (2^-25 turns, 2^-22.3 rad), sine and cosine are off by at most 2 ulp
+# (2^-23 each), mscale and the two products and the sum round once each (2^-24): below 2^-21 of |a| + |b|.
+# A position p adds |p| 2^-53 turns of a double frequency (here and in the formula): 2^-21 at |p| = 2^31.
+ROT_TOL = 2.0 ** -21
+
+
+def _rope_tol(mag, want, dtype, pos=None):
+    far = 0.0 if pos is None else float(pos.double().abs().max()) * 2.0 ** -50
+    return (ROT_TOL + far) * mag + HALF[dtype] * want.abs()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype,cache", [(F32, BF16), (BF16, BF16), (F32, F32), (BF16, F32)])
+@pytest.mark.parametrize("T,S,hq,hkv,hd,rot", [(1, 1, 16, 16, 128, 128), (193, 193, 32, 8, 128, 96), (700, 3, 4, 4, 64, 64),
+                                               (37, 5, 7, 1, 80, 22), (3000, 2, 2, 2, 256, 2), (9, 9, 1, 1, 16, 16)])
+def test_rope_append(spd, layout, dtype, cache, T, S, hq, hkv, hd, rot):
+    g = _g(T + hd)
+    cap = -(-T // S) + 5
+    qkv = _rn(g, T, (hq + 2 * hkv) * hd, dtype=dtype)
+    q, k, v = (x.unflatten(1, (-1, hd)) for x in qkv.split([hq * hd, hkv * hd, hkv * hd], dim=1))
+    i = torch.arange(T, device="cuda")
+    seq, slot = (i % S).int(), (2 + i // S).int()
+    pos = torch.randint(-5000, 300000, (T,), generator=g, device="cuda").int()
+    slot[::7] = torch.tensor([-1, cap, -(2 ** 31), 2 ** 31 - 1], device="cuda", dtype=torch.int32)[(i[::7] % 4)]
+    if T > 2:
+        seq[2] = S
+    kc, vc = _rn(g, S, hkv, cap, hd, dtype=cache), _rn(g, S, hkv, cap, hd, dtype=cache)
+    kc0, vc0 = kc.clone(), vc.clone()
+    q_out = torch.full((T, hq, hd), float("nan"), dtype=dtype, device="cuda")
+    rope = spd.Rope(hd, rot_dim=rot, layout=layout)
+    spd.rope_append(rope, q, q_out, pos, k=k, v=v, k_cache=kc, v_cache=vc, slot=slot, seq=seq)
+    f, m = _freqs(rot)
+    want, mag = _rot64(q, pos, f, m, rot, layout)
+    _close(q_out, want, _rope_tol(mag, want, dtype, pos))
+    keep = ((slot >= 0) & (slot < cap) & (seq < S)).nonzero()[:, 0]
+    at = (seq[keep].long(), slice(None), slot[keep].long())
+    want, mag = _rot64(k, pos, f, m, rot, layout)
+    _close(kc[at], want[keep], _rope_tol(mag, want, cache, pos)[keep])
+    assert torch.equal(vc[at], v[keep].to(cache))
+    kc[at], vc[at] = kc0[at], vc0[at]  # nothing else was touched
+    assert torch.equal(kc, kc0) and torch.equal(vc, vc0)
+
+
+@pytest.mark.parametrize("scaling,factor,theta,rot", [("linear", 4.0, 10000.0, 128), ("ntk", 8.0, 10000.0, 64), ("ntk", 8.0, 10000.0, 2),
+                                                      ("yarn", 8.0, 10000.0, 128), ("yarn", 32.0, 500000.0, 96), ("yarn", 1.0, 10000.0, 64),
+                                                      ("yarn", 2.0, 1.5, 32)])
+def test_rope_scalings(spd, scaling, factor, theta, rot):
+    g = _g(3)
+    q = _rn(g, 11, 3, 128)
+    pos = torch.tensor([0, 1, -1, 2047, 32768, 262143, 1000003, 2 ** 31 - 1, -(2 ** 31), 7, 123456789], dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    spd.rope_append(spd.Rope(128, rot, theta=theta, scaling=scaling, factor=factor, original_context=32768), q, out, pos)
+    f, m = _freqs(rot, theta, scaling, factor, 32768)
+    want, mag = _rot64(q, pos, f, m, rot, "half")
+    for i in range(len(pos)):
+        _close(out[i], want[i], _rope_tol(mag, want, F32, pos[i])[i])
+    assert torch.equal(out[..., rot:], q[..., rot:]) and torch.equal(out[0, :, :rot] if m == 1 else out[0, :, rot:],
+                                                                      q[0, :, :rot] if m == 1 else q[0, :, rot:])
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rope_unaligned_rows_in_place_and_streams(spd, layout, dtype):
+    """Rows that start at odd elements take the scalar path and give what aligned ones do; in place; on another stream."""
+    g = _g(4)
+    T, hq, hd = 33, 5, 64
+    q = _rn(g, T, hq, hd, dtype=dtype)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 911
+    want = torch.empty_like(q)
+    rope = spd.Rope(hd, layout=layout)
+    spd.rope_append(rope, q, want, pos)
+    wide = torch.zeros(T, hq * hd + 3, dtype=dtype, device="cuda")
+    view = wide[:, 1: 1 + hq * hd].unflatten(1, (hq, hd))
+    view.copy_(q)
+    spd.rope_append(rope, view, view, pos)
+    assert torch.equal(view, want)
+    assert not wide[:, 0].any() and not wide[:, -2:].any()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    inplace = q.clone()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        spd.rope_append(rope, inplace, inplace, pos)  # torch's current stream
+    s.synchronize()
+    assert torch.equal(inplace, want)
+
+
+def test_rope_keys_alone_one_sequence_and_no_tokens(spd):
+    g = _g(5)
+    T, hkv, hd, cap = 6, 2, 64, 9
+    k, v = _rn(g, T, hkv, hd), _rn(g, T, hkv, hd)
+    kc, vc = torch.zeros(hkv, cap, hd, dtype=BF16, device="cuda"), torch.zeros(hkv, cap, hd, dtype=BF16, device="cuda")
+    pos, slot = torch.arange(T, dtype=torch.int32, device="cuda"), torch.arange(T, dtype=torch.int32, device="cuda") + 3
+    rope = spd.Rope(hd)
+    spd.rope_append(rope, None, None, pos, k=k, v=v, k_cache=kc, v_cache=vc, slot=slot)
+    f, m = _freqs(hd)
+    want, mag = _rot64(k, pos, f, m, hd, "half")
+    _close(kc[:, 3:], want.transpose(0, 1), _rope_tol(mag, want, BF16).transpose(0, 1))
+    assert torch.equal(vc[:, 3:], v.to(BF16).transpose(0, 1)) and not kc[:, :3].any()
+    e = torch.empty(0, dtype=torch.int32, device="cuda")
+    spd.rope_append(rope, torch.empty(0, 3, hd, device="cuda"), torch.empty(0, 3, hd, device="cuda"), e)
+    # all tokens are padding
+    before = kc.clone()
+    spd.rope_append(rope, None, None, pos, k=k, v=v, k_cache=kc, v_cache=vc, slot=torch.full_like(slot, -1))
+    assert torch.equal(kc, before)
+
+
+# ---------------------------------------------------------------------------------------------
+# 4-bit products
+# ---------------------------------------------------------------------------------------------
+def _unpack(codes, scales, zeros):
+    """Weights in 64 bits."""
+    rows, cols = codes.size(0), codes.size(1) * 2
+    group = cols // scales.size(1)
+    q = torch.stack([codes & 15, codes >> 4], 2).view(rows, -1, group).double()
+    return ((q - (8 if zeros is None else zeros.double()[..., None])) * scales.double()[..., None]).view(rows, cols)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale_dtype", [F32, BF16])
+@pytest.mark.parametrize("symmetric", [True, False])
+@pytest.mark.parametrize("rows,cols,group", [(1, 32, 32), (37, 192, 64), (300, 1408, 128)])
+def test_q4_quantize(spd, dtype, scale_dtype, symmetric, rows, cols, group):
+    w = _rn(_g(rows), rows, cols, dtype=dtype, std=0.02)
+    w[0, :group] = 0  # a group of scale 0
+    if rows > 1:
+        w[1] = w[1].abs() + 0.01
+        w[2] = -w[2].abs() - 0.01
+    codes, scales, zeros = spd.q4_quantize(w, group, symmetric, scale_dtype)
+    x = w.float().view(rows, -1, group)
+    if symmetric:
+        s = (x.abs().amax(2).double() / 7).float().to(scale_dtype)
+        z = torch.full_like(s, 8, dtype=F32)
+    else:
+        hi, lo = x.amax(2).clamp(min=0), x.amin(2).clamp(max=0)
+        s = ((hi - lo).double() / 15).float().to(scale_dtype)
+        z = torch.where(s > 0, torch.round(-lo / s.float()).clamp(0, 15), 0)
+    code = (torch.where(s.float()[..., None] > 0, torch.round(x / s.float()[..., None]), 0) + z[..., None]).clamp(0, 15)
+    assert torch.equal(scales, s)
+    assert zeros is None if symmetric else torch.equal(zeros.float(), z)
+    c = torch.stack([codes & 15, codes >> 4], 2).view(rows, -1, group)
+    assert torch.equal(c.float(), code)
+    # half a step from the weight, and a rounded scale's 15 half steps, except where the ends are cut off
+    err = (_unpack(codes, scales, zeros) - w.double()).abs().view(rows, -1, group)
+    assert (err <= s.double()[..., None] * (0.5 + 15 * HALF[scale_dtype] + (0 if symmetric else 0.5)) + 1e-12).all()
+
+
+def _check_gemv(spd, shapes, cols, group, scale_dtype, zeros, M, dtype, norm, seed=0, spread=False):
+    g = _g(seed + cols + M)
+    raw, Ws = [], []
+    for rows in shapes:
+        w = _rn(g, rows, cols, std=0.02)
+        c, s, z = spd.q4_quantize(w, group, not zeros, scale_dtype)
+        raw.append(_unpack(c, s, z))
+        Ws.append(spd.q4_pack(c, s, z))
+    x = _rn(g, M, cols)
+    if spread:  # magnitudes over many powers of two
+        x = x * torch.exp2(torch.randint(-12, 12, (M, cols), generator=g, device="cuda"))
+    x = x.to(dtype)
+    nw = 1 + 0.1 * _rn(g, cols) if norm else None
+    ys = [torch.full((M, r), float("nan"), dtype=dtype, device="cuda") for r in shapes]
+    spd.q4_gemv(Ws, [x] * len(Ws), ys, norm_weight=nw)
+    xx = x.double()
+    if norm:
+        xx = xx * torch.rsqrt(xx.square().mean(1, keepdim=True) + 1e-6) * nw.double()
+    for W, y in zip(raw, ys):
+        want, mag = xx @ W.T, xx.abs() @ W.abs().T
+        # 16 products at a time, a scale and a sum per group, the joins of warps; the norm: its sum of squares, one
+        # product and two bf16 terms (2^-16) where the vectors are bf16
+        tol = (cols / 16 + cols / group + 64 + (cols / 128 + 8 if norm else 0)) * U
+        if norm and dtype == BF16:
+            tol += 2.0 ** -16
+        _close(y, want, tol * mag + HALF[dtype] * want.abs())
+    return Ws, x, ys
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shapes,cols,group,scale_dtype,zeros,M,norm", [
+    ((4096, 1024, 1024), 4096, 128, BF16, False, 1, True),
+    ((2049, 37), 5632, 32, F32, True, 5, False),
+    ((1,), 32, 32, BF16, True, 1, False),            # one row, a quarter of a column block
+    ((15, 16, 17), 96, 32, F32, False, 2, True),     # rows around a tile, three quarters of a block
+    ((300,), 192, 64, BF16, True, 3, True),          # a block and a half
+    ((1000, 1), 12288, 128, BF16, False, 16, False),
+    ((640,), 12288, 64, F32, True, 32, True),        # the most vectors, wide: several passes of vectors
+    ((64,), 32768, 128, BF16, False, 7, False),      # the widest
+    ((5000,), 2560, 128, BF16, True, 8, False),
+    ((48,) * 34, 256, 128, F32, False, 4, True),     # the most matrices
+    ((151936,), 256, 128, BF16, False, 1, False),
+])
+def test_q4_gemv(spd, dtype, shapes, cols, group, scale_dtype, zeros, M, norm):
+    _check_gemv(spd, shapes, cols, group, scale_dtype, zeros, M, dtype, norm)
+
+
+@pytest.mark.parametrize("M", list(range(1, 33)))
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_q4_gemv_every_count_of_vectors(spd, M, dtype):
+    _check_gemv(spd, (100,), 1024, 64, BF16, True, M, dtype, M % 2 == 0, spread=True)
+
+
+def test_q4_gemv_strides_shared_and_own_vectors(spd):
+    """Parts of fused rows as inputs and outputs, a vector per matrix, single vectors without a batch dimension."""
+    g = _g(9)
+    cols, M = 512, 3
+    Ws, raw = [], []
+    for rows in (64, 40, 40):
+        c = spd.q4_quantize(_rn(g, rows, cols, std=0.02), 128)
+        raw.append(_unpack(*c))
+        Ws.append(spd.q4_pack(*c))
+    xw = _rn(g, M, cols + 7)
+    x0, x1 = xw[:, :cols], xw[:, 7:]
+    yw = torch.full((M, 64 + 40 + 40 + 1), float("nan"), device="cuda")
+    ys = [yw[:, 0:64], yw[:, 64:104], yw[:, 105:145]]
+    spd.q4_gemv(Ws, [x0, x0, x1], ys)
+    for W, x, y in zip(raw, (x0, x0, x1), ys):
+        _close(y, x.double() @ W.T, (cols / 16 + 80) * U * (x.double().abs() @ W.abs().T) + 1e-30)
+    assert torch.isnan(yw[:, 104]).all()
+    y1 = torch.empty(64, device="cuda")
+    spd.q4_gemv([Ws[0]], [x0[1].contiguous()], [y1])
+    assert torch.equal(y1, ys[0][1]) or (y1 - ys[0][1]).abs().max() <= 40 * U * float((x0[1].abs().double() @ raw[0].abs().T).max())
+
+
+def test_q4_gemv_infinities_and_nan_stay_in_their_vector(spd):
+    g = _g(10)
+    c = spd.q4_quantize(_rn(g, 50, 256, std=0.02), 128)
+    W = spd.q4_pack(*c)
+    x = _rn(g, 4, 256)
+    x[1, 17], x[2, 200], x[3] = float("nan"), float("inf"), 3.0e38
+    y = torch.empty(4, 50, device="cuda")
+    spd.q4_gemv([W], [x], [y])
+    want = x[0].double() @ _unpack(*c).T
+    _close(y[0], want, 100 * U * (x[0].double().abs() @ _unpack(*c).abs().T))
+    assert torch.isnan(y[1]).all()
+    col = _unpack(*c)[:, 200]
+    assert torch.equal(y[2] == float("inf"), col > 0) and torch.equal(y[2] == float("-inf"), col < 0)
+
+
+# ---------------------------------------------------------------------------------------------
+# shared-prefix attention
+# ---------------------------------------------------------------------------------------------
+def _attn64(q, pk, pv, P, kc, vc, lens):
+    """(out, lse, tolerance of out for fp32 queries, sum p |v|) in 64 bits."""
+    B, hq, hd = q.shape
+    hkv = (pk if pk is not None else kc).size(-3)
+    G = hq // hkv
+    out = torch.zeros(B, hq, hd, dtype=torch.float64, device="cuda")
+    mag, tol = out.clone(), torch.zeros(B, hq, dtype=torch.float64, device="cuda")
+    lse = torch.full((B, hq), -math.inf, dtype=torch.float64, device="cuda")
+    for b in range(B):
+        n = int(lens[b]) if lens is not None else 0
+        for h in range(hkv):
+            ks = [x for x in ((pk[h, :P] if P else None), (kc[b, h, :n] if n else None)) if x is not None]
+            vs = [x for x in ((pv[h, :P] if P else None), (vc[b, h, :n] if n else None)) if x is not None]
+            if not ks:
+                continue
+            K, V, Q = torch.cat(ks).double(), torch.cat(vs).double(), q[b, h * G:(h + 1) * G].double()
+            s = Q @ K.T / math.sqrt(hd)
+            p = torch.softmax(s, 1)
+            sl = slice(h * G, (h + 1) * G)
+            out[b, sl], mag[b, sl], lse[b, sl] = p @ V, p @ V.abs(), s.logsumexp(1)
+            # the scores' sums (three terms, 16 products at a time), their scale and exponent; then the keys' sums
+            d = (Q.abs() @ K.abs().T / math.sqrt(hd)).amax(1)
+            tol[b, sl] = 2 * d * (3 * hd / 16 + 8) * U + (len(K) / 16 + 64) * U + 2.0 ** -20
+    return out, lse, tol, mag
+
+
+def _run_attn(spd, q, pk, pv, P, kc, vc, lens, want_lse=True, stream=None, ws=None):
+    B, hq, hd = q.shape
+    hkv = (pk if pk is not None else kc).size(-3)
+    n = spd.shared_prefix_attention_workspace_bytes(B, hq, hkv, hd, P)
+    assert n > 0
+    if ws is None:
+        ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # NaN everywhere: no initialisation is needed
+    out = torch.full_like(q, float("nan"))
+    lse = torch.full((B, hq), float("nan"), device="cuda") if want_lse else None
+    spd.shared_prefix_attention(q, pk, pv, P, kc, vc, lens, out, ws, lse=lse, stream=stream)
+    return out, lse
+
+
+def _check_attn(spd, B, P, cap, hq, hkv, hd, dtype, lens=None, extra=0, std=1.5, seed=0):
+    g = _g(seed + B + P + cap)
+    q = _rn(g, B, hq, hd, dtype=dtype, std=std)
+    pk, pv = _rn(g, hkv, P + extra, hd, dtype=BF16), _rn(g, hkv, P + extra, hd, dtype=BF16)
+    pk[:, P:], pv[:, P:] = float("nan"), float("inf")
+    kc, vc = _rn(g, B, hkv, cap, hd, dtype=BF16), _rn(g, B, hkv, cap, hd, dtype=BF16)
+    if lens is None:
+        lens = torch.randint(0, cap + 1, (B,), generator=g, device="cuda").int()
+        lens[0] = cap
+        if B > 1:
+            lens[1] = 0
+    else:
+        lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    there = (torch.arange(cap, device="cuda") < lens[:, None])[:, None, :, None]
+    kc, vc = torch.where(there, kc, float("nan")), torch.where(there, vc, float("-inf"))  # what lies behind is not used
+    out, lse = _run_attn(spd, q, pk, pv, P, kc, vc, lens)
+    want, wl, tol, mag = _attn64(q, pk, pv, P, kc, vc, lens)
+    t = tol[..., None] * mag + HALF[dtype] * want.abs()
+    if dtype == BF16:
+        t = t + 2.0 ** -8 * mag  # the probabilities are rounded to bf16
+    _close(out, want, t)
+    _close(lse, wl, tol + 2.0 ** -22 * wl.abs().nan_to_num(posinf=0.0, neginf=0.0))
+    return out, lse
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,P,cap,hq,hkv,hd", [
+    (1, 37, 16, 16, 16, 128), (17, 1111, 300, 16, 16, 128), (32, 2048, 64, 32, 8, 128), (3, 1, 1, 4, 4, 64), (2, 127, 33, 28, 4, 128),
+    (70, 129, 5, 14, 2, 64), (5, 5000, 40, 8, 1, 128), (1, 9000, 3, 12, 1, 64), (300, 300, 2, 2, 2, 64), (33, 4096, 17, 32, 8, 128),
+    (65, 640, 65, 40, 2, 128), (2, 16, 2500, 8, 2, 128), (1, 128, 7000, 8, 8, 64), (129, 256, 1, 8, 8, 128)])
+def test_shared_prefix_attention(spd, dtype, B, P, cap, hq, hkv, hd):
+    _check_attn(spd, B, P, cap, hq, hkv, hd, dtype, extra=3)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("P", [1, 15, 16, 17, 31, 63, 64, 65, 126, 127, 128, 129, 255, 256, 257, 383, 511, 513, 1023, 1025])
+def test_shared_prefix_attention_every_end(spd, dtype, P):
+    _check_attn(spd, 6, P, 140, 8, 2, 64 if P % 2 else 128, dtype, lens=[0, 1, 16, 33, 128, 139], extra=P % 5)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_shared_prefix_attention_large_scores(spd, dtype):
+    """Scores of +-100: one key carries the row; earlier parts are scaled away."""
+    _check_attn(spd, 9, 700, 50, 8, 2, 128, dtype, std=30.0)
+
+
+def test_shared_prefix_attention_empty_rows_and_bad_lengths(spd):
+    g = _g(11)
+    q = _rn(g, 5, 4, 64)
+    kc, vc = _rn(g, 5, 2, 8, 64, dtype=BF16), _rn(g, 5, 2, 8, 64, dtype=BF16)
+    lens = torch.tensor([0, 8, -1, 9, 3], dtype=torch.int32, device="cuda")
+    for P in (0, 40):
+        pk, pv = (_rn(g, 2, P, 64, dtype=BF16), _rn(g, 2, P, 64, dtype=BF16)) if P else (None, None)
+        out, lse = _run_attn(spd, q, pk, pv, P, kc, vc, lens)
+        good = torch.tensor([0, 1, 4], device="cuda")
+        want, wl, tol, mag = _attn64(q[good], pk, pv, P, kc[good], vc[good], lens[good])
+        _close(out[good], want, tol[..., None] * mag + 1e-30)
+        _close(lse[good], wl, tol + 1e-6)
+        assert torch.isnan(out[2:4]).all() and torch.isnan(lse[2:4]).all()
+        if P == 0:
+            assert (out[0] == 0).all() and (lse[0] == -math.inf).all()
+    # no caches at all, and no lse
+    out, _ = _run_attn(spd, q, pk, pv, 40, None, None, None, want_lse=False)
+    want, _, tol, mag = _attn64(q, pk, pv, 40, None, None, None)
+    _close(out, want, tol[..., None] * mag + 1e-30)
+    # a cache without room, and a prefix buffer of which nothing is used
+    e = kc[:, :, :0].contiguous()
+    out, lse = _run_attn(spd, q, pk, pv, 0, e, e, torch.zeros(5, dtype=torch.int32, device="cuda"))
+    assert (out == 0).all() and (lse == -math.inf).all()
+
+
+def test_shared_prefix_attention_nan_keys_stay_in_their_rows(spd):
+    """A NaN among the keys in use makes the rows that see it NaN, and no other."""
+    g = _g(12)
+    q = _rn(g, 3, 4, 64)
+    pk, pv = _rn(g, 2, 200, 64, dtype=BF16), _rn(g, 2, 200, 64, dtype=BF16)
+    kc, vc = _rn(g, 3, 2, 20, 64, dtype=BF16), _rn(g, 3, 2, 20, 64, dtype=BF16)
+    lens = torch.tensor([20, 10, 5], dtype=torch.int32, device="cuda")
+    kc[1, 0, 3, 5] = float("nan")
+    pk[1, 150, 0] = float("nan")
+    out, _ = _run_attn(spd, q, pk, pv, 200, kc, vc, lens)
+    nan = torch.isnan(out).all(2)
+    assert torch.equal(torch.isnan(out).any(2), nan)
+    assert nan.cpu().tolist() == [[False, False, True, True], [True, True, True, True], [False, False, True, True]]
+
+
+def test_shared_prefix_attention_repeats_bit_for_bit_and_on_two_streams(spd):
+    g = _g(13)
+    B, P, hq, hkv, hd = 24, 3000, 16, 4, 128
+    q = _rn(g, B, hq, hd, dtype=BF16)
+    pk, pv = _rn(g, hkv, P, hd, dtype=BF16), _rn(g, hkv, P, hd, dtype=BF16)
+    kc, vc = _rn(g, B, hkv, 40, hd, dtype=BF16), _rn(g, B, hkv, 40, hd, dtype=BF16)
+    lens = torch.randint(0, 41, (B,), generator=g, device="cuda").int()
+    want, wl = _run_attn(spd, q, pk, pv, P, kc, vc, lens)
+    torch.cuda.synchronize()
+    ss = [torch.cuda.Stream() for _ in range(2)]
+    n = spd.shared_prefix_attention_workspace_bytes(B, hq, hkv, hd, P)
+    wss = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in ss]
+    got = []
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, ws in zip(ss, wss):
+            with torch.cuda.stream(s):
+                got.append(_run_attn(spd, q, pk, pv, P, kc, vc, lens, ws=ws))
+    torch.cuda.synchronize()
+    for o, l in got:
+        assert torch.equal(o, want) and torch.equal(l, wl)
+
+
+def test_offsets_beyond_32_bits(spd):
+    """Caches of more than 2^32 elements: the last sequences' rows are read and written."""
+    B, hkv, cap, hd, hq = 3, 8, 1 << 21, 128, 8  # 6.4e9 elements, 12.9 GB a cache
+    kc = torch.empty(B, hkv, cap, hd, dtype=BF16, device="cuda")
+    vc = torch.empty(B, hkv, cap, hd, dtype=BF16, device="cuda")
+    g = _g(14)
+    n = 100
+    base = cap - n
+    q, k, v = _rn(g, n, hq, hd), _rn(g, n, hkv, hd), _rn(g, n, hkv, hd)
+    i = torch.arange(n, dtype=torch.int32, device="cuda")
+    rope = spd.Rope(hd)
+    out = torch.empty_like(q)
+    spd.rope_append(rope, q, out, i, k=k, v=v, k_cache=kc, v_cache=vc, slot=i + base, seq=torch.full_like(i, B - 1))
+    f, m = _freqs(hd)
+    want, mag = _rot64(k, i, f, m, hd, "half")
+    _close(kc[B - 1, :, base:], want.transpose(0, 1), _rope_tol(mag, want, BF16).transpose(0, 1))
+    assert torch.equal(vc[B - 1, :, base:], v.to(BF16).transpose(0, 1))
+    kc[B - 1, :, :n], vc[B - 1, :, :n] = k.to(BF16).transpose(0, 1), v.to(BF16).transpose(0, 1)
+    lens = torch.tensor([0, 0, n], dtype=torch.int32, device="cuda")
+    pk = pv = torch.zeros(hkv, 1, hd, dtype=BF16, device="cuda")
+    got, _ = _run_attn(spd, q[:B].contiguous(), pk, pv, 1, kc, vc, lens)
+    want, _, tol, mag = _attn64(q[:B], pk, pv, 1, kc, vc, lens)
+    _close(got, want, tol[..., None] * mag + 1e-30)
+
+
+# ---------------------------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------------------------
+def _block(spd, st):
+    """One decode step's attention block: 4-bit QKV with the norm, rotary positions and append, attention, 4-bit output."""
+    hd, hq, hkv = st["hd"], st["hq"], st["hkv"]
+    parts = st["qkv"].split([hq * hd, hkv * hd, hkv * hd], dim=1)
+    spd.q4_gemv(st["W"][:3], [st["x"]] * 3, parts, norm_weight=st["nw"])
+    q, k, v = (p.unflatten(1, (-1, hd)) for p in parts)
+    spd.rope_append(st["rope"], q, st["q"], st["pos"], k=k, v=v, k_cache=st["kc"], v_cache=st["vc"], slot=st["lens"], seq=st["seq"])
+    st["lens"] += 1
+    st["pos"] += 1
+    spd.shared_prefix_attention(st["q"], st["pk"], st["pv"], st["P"], st["kc"], st["vc"], st["lens"], st["o"], st["ws"])
+    spd.q4_gemv(st["W"][3:], [st["o"].flatten(1)], [st["y"]])
+
+
+def _block_state(spd, dtype, B=13, P=300, hq=8, hkv=2, hd=128, d=512, cap=12):
+    g = _g(21)
+    raw = [spd.q4_quantize(_rn(g, r, c, std=0.05), 128) for r, c in
+           ((hq * hd, d), (hkv * hd, d), (hkv * hd, d), (d, hq * hd))]
+    st = dict(hd=hd, hq=hq, hkv=hkv, P=P, raw=raw, W=[spd.q4_pack(*r) for r in raw], x=_rn(g, B, d, dtype=dtype), nw=1 + 0.1 * _rn(g, d),
+              qkv=torch.empty(B, (hq + 2 * hkv) * hd, dtype=dtype, device="cuda"), rope=spd.Rope(hd, scaling="yarn", factor=4.0, original_context=200),
+              q=torch.empty(B, hq, hd, dtype=dtype, device="cuda"), pk=_rn(g, hkv, P, hd, dtype=BF16), pv=_rn(g, hkv, P, hd, dtype=BF16),
+              kc=_rn(g, B, hkv, cap, hd, dtype=BF16), vc=_rn(g, B, hkv, cap, hd, dtype=BF16),
+              lens=torch.randint(0, cap - 4, (B,), generator=g, device="cuda").int(), seq=torch.arange(B, dtype=torch.int32, device="cuda"),
+              o=torch.empty(B, hq, hd, dtype=dtype, device="cuda"), y=torch.empty(B, d, dtype=dtype, device="cuda"),
+              ws=torch.empty(spd.shared_prefix_attention_workspace_bytes(B, hq, hkv, hd, P), dtype=torch.uint8, device="cuda"))
+    st["pos"] = st["lens"] + P
+    return st
+
+
+@pytest.mark.parametrize("dtype,tol", [(F32, 1e-2), (BF16, 3e-2)])
+def test_decode_block_against_formulas(spd, dtype, tol):
+    """Three steps.  Keys and values pass through a bf16 cache, which may round a borderline value the other way than the
+    formula (2^-8 of it), and bf16 activations round at each of five hand-overs: the bounds are on the result's norm."""
+    st = _block_state(spd, dtype)
+    kc, vc = st["kc"].double(), st["vc"].double()
+    lens, pos = st["lens"].clone(), st["pos"].clone()
+    W = [_unpack(*r) for r in st["raw"]]
+    f, m = _freqs(128, 10000.0, "yarn", 4.0, 200)
+    B = len(lens)
+    i = torch.arange(B, device="cuda")
+    for step in range(3):
+        _block(spd, st)
+        x = st["x"].double()
+        x = x * torch.rsqrt(x.square().mean(1, keepdim=True) + 1e-6) * st["nw"].double()
+        q, k, v = ((x @ w.T).unflatten(1, (-1, 128)) for w in W[:3])
+        q, k = _rot64(q, pos, f, m, 128, "half")[0], _rot64(k, pos, f, m, 128, "half")[0]
+        kc[i, :, lens.long()], vc[i, :, lens.long()] = k.to(BF16).double(), v.to(BF16).double()
+        lens, pos = lens + 1, pos + 1
+        o = _attn64(q, st["pk"], st["pv"], st["P"], kc, vc, lens)[0]
+        y = o.flatten(1) @ W[3].T
+        assert torch.equal(st["lens"], lens) and torch.equal(st["pos"], pos)
+        assert float((st["y"].double() - y).norm() / y.norm()) < tol
+        st["x"].copy_(st["y"])
+
+
+def test_decode_block_captured_and_replayed(spd):
+    """A captured block replays with lengths, positions and caches that move on the device, like eager calls."""
+    eager, graph = _block_state(spd, BF16), _block_state(spd, BF16)
+    warm = _block_state(spd, BF16)
+    _block(spd, warm)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        _block(spd, graph)
+    for step in range(4):
+        _block(spd, eager)
+        g.replay()
+        torch.cuda.synchronize()
+        for name in ("y", "kc", "vc", "lens", "pos", "q", "o"):
+            assert torch.equal(eager[name], graph[name]), (step, name)
