@@ -4,17 +4,33 @@
 // the sequence's own keys 0..len-1: the softmax is taken in one pass with a running maximum and sum, over parts of the
 // keys, and the parts (O, m, l) are joined as  O = sum_i O_i e^(m_i - m),  l = sum_i l_i e^(m_i - m).
 //
-// rows kernel: one block per (sequence, kv head, up to 8 query heads of its group).  Its warps take 32 keys in turn and
+// prefix kernel (tcgen05): the queries of one kv head, all sequences' together, are the 128 rows of an MMA tile:
+//   S = Q K_c^T  (M 128 x N 128 keys x K hd, fp32 in TMEM);  P = exp2(S - m) goes back to TMEM as bf16, over S, and is the A
+//   operand of  O += P V_c  (M 128 x N hd x K 128 keys).
+// One thread per row holds the row's 128 scores in registers, its running maximum and sum.  O is rescaled only when the
+// maximum has grown by more than 8 (a factor of 256, which bf16's and fp32's exponents take without loss), so nearly never
+// after the first chunk.  K and V chunks of 128 keys come by TMA through a ring of shared-memory stages; the tensor maps end
+// at the prefix's length, so that rows beyond it are zeros whatever the buffer holds.  bf16 queries: two tiles a block
+// alternate, one in the tensor core while the other's softmax runs.  fp32 queries: one tile, Q and P as three bf16 terms.
+// The work, (row tiles) x (chunks), is cut into equal runs, one per SM; a run that crosses from one tile to the next leaves
+// a part for each.  A chunk (64 KB at hd 128) feeds 2 x 4.2 MMAC a tile: the memory bounds up to about 256 rows a kv head,
+// the tensor cores and exponentials beyond.
+//
+// rows kernel: joins those parts with the sequence's own keys.  One block per (sequence, kv head, up to 8 query heads of its group).  Its warps take 32 keys in turn and
 // work on mma.sync m16n8k16: S^T = K Q^T (16 keys x 8 heads), then O^T += V^T P^T (16 head elements x 8 heads).  K and V go
 // from global memory straight into operand registers: the order of the head elements in a dot product is free, so a lane
 // reads 16 consecutive bytes; V's pairs of keys are put together with byte permutes.  fp32 queries and their
 // probabilities enter as three bf16 terms (exact), bf16 queries' probabilities as one (rounded to bf16, 2^-9 relative,
 // like the output).  Statistics and sums are fp32.
+#include <cudaTypedefs.h>
+
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <mutex>
 
 #include "spd_internal.cuh"
+#include "spd_tc.cuh"
 
 namespace spd {
 namespace spa {
@@ -30,11 +46,18 @@ struct Params {
   const int* lens;
   void* out;
   float* lse;
-  float* part;
+  float* part;      // prefix parts: unnormalised O [slot][row of the unit][hd]
+  float2* part_ml;  // their maximum and sum [slot][row of the unit]
   long long prefix_cap, max_seq;
   int P, B, hq, hkv, gq, hblocks;
   float scale_log2;  // log2(e) / sqrt(hd)
+  // prefix kernel: `units` row tiles (pairs) x nch chunks, cut into n_cta runs; the part of run i for unit u is slot i + u
+  int units_per_kv, units, nch, n_cta;
+  int use_prefix;
 };
+
+// first chunk of run i
+__host__ __device__ inline long long run_start(long long total, int n, int i) { return total * i / n; }
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -60,8 +83,395 @@ __device__ __forceinline__ uint32_t take_pair(float& a, float& b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One 16-key step of the keys at `k0`, `n` of them in range (the others repeat the last one and weigh nothing).
-template <int HD> struct KeyRegs { uint4 v[2][HD / 32]; };
+
+// ---------------------------------------------------------------------------------------------
+// prefix kernel
+// ---------------------------------------------------------------------------------------------
+constexpr int kTile = 128;   // rows of a tile, keys of a chunk
+template <int HD, int TERMS> struct Cfg {
+  static constexpr int kSlots = TERMS == 1 ? 2 : 1;              // row tiles of a block
+  static constexpr int kTB = HD / 64 * kTile * 128;              // bytes of a 128-row operand
+  static constexpr int kQ = kSlots * TERMS * kTB;                // Q
+  static constexpr int kStages = (227 * 1024 - 2048 - kQ) / kTB > 8 ? 8 : (227 * 1024 - 2048 - kQ) / kTB;
+  static constexpr int kSmem = 1024 + kQ + kStages * kTB;
+  // softmax warps, a copying and a multiplying warp; two tiles: a whole third warpgroup, which gives up registers
+  static constexpr int kThreads = kSlots == 2 ? 384 : 192;
+  // TMEM columns: two tiles: S0 S1 O0 O1, P over S; one tile: S, O, and three P
+  static constexpr uint32_t s_col(int i) { return 128u * i; }
+  static constexpr uint32_t o_col(int i) { return kSlots == 2 ? 256u + 128u * i : 128u; }
+  static constexpr uint32_t p_col(int i) { return kSlots == 2 ? 128u * i : 256u; }
+};
+
+struct PrefixMaps {
+  CUtensorMap k, v;
+};
+
+__device__ __forceinline__ void tma3(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t db, uint32_t id, bool accumulate) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+               " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(db), "r"(id),
+               "r"((uint32_t)accumulate)
+               : "memory");
+}
+// V as the second operand, keys along K: rows of 128 bytes, 8-key groups 1024 B apart, the halves of hd one tile apart
+__device__ __forceinline__ uint64_t desc_v(uint32_t a) {
+  return (uint64_t)((a & 0x3FFFFu) >> 4) | ((uint64_t)((kTile * 128) >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__host__ __device__ constexpr uint32_t idesc(int n, int b_mn_major) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(kTile >> 4) << 24);
+}
+__device__ __forceinline__ void tm_st32(uint32_t ta, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      ::"r"(ta), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+        "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+        "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t ta, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+               ::"r"(ta), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+                 "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+               : "memory");
+}
+__device__ __forceinline__ void tm_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void opaque(uint64_t& x) { asm volatile("" : "+l"(x)); }
+
+// Byte offset of element (row r, column e) in a [64-element chunk][128 rows][128 B] operand with the 128-byte swizzle.
+__device__ __forceinline__ uint32_t swz(int r, int e) {
+  return (uint32_t)((e >> 6) * (kTile * 128) + r * 128 + ((((e & 63) >> 3) ^ (r & 7)) << 4) + (e & 7) * 2);
+}
+
+// Bounded wait that also ends once another role of the block has given up.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 0;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 63u && (*fail || globaltimer_ns() - t0 > kWaitLimitNs)) {
+      *fail = 1;
+      return false;
+    }
+  }
+}
+
+template <int HD, int TERMS>
+__global__ void __launch_bounds__(Cfg<HD, TERMS>::kThreads, 1)
+prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMaps maps) {
+  using C = Cfg<HD, TERMS>;
+  constexpr int NS = C::kSlots, ST = C::kStages;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* sq = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  unsigned char* ring = sq + C::kQ;
+  __shared__ __align__(8) uint64_t full[ST], empty[ST], q_ready[NS], s_full[NS], p_ready[NS], o_full[NS], s_free[NS], pv_done, drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_fail_;
+  volatile int& s_fail = *const_cast<volatile int*>(&s_fail_);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  constexpr int kCopyWarp = NS * 4, kMmaWarp = NS * 4 + 1;
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&q_ready[i], 128);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_ready[i], 128);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&s_free[i], 128);
+    }
+    mbar_init(&pv_done, 1);
+    mbar_init(&drain, 1);
+    s_fail_ = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tc::alloc_cols(&s_tmem, 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  pdl_trigger();  // the rows kernel may start its own keys beside this one
+  const uint32_t tm = s_tmem;
+  const long long total = (long long)p.units * p.nch;
+  const long long w0 = run_start(total, p.n_cta, blockIdx.x), w1 = run_start(total, p.n_cta, blockIdx.x + 1);
+  const int rows = p.B * p.gq;
+
+  // a piece: the chunks [c0, c1) of one unit; the unit's tiles with rows
+  struct Piece { int u, c0, c1, kh, row0, nt; };
+  auto piece_at = [&](long long w) {
+    Piece x;
+    x.u = (int)(w / p.nch);
+    x.c0 = (int)(w - (long long)x.u * p.nch);
+    x.c1 = (int)min((long long)p.nch, x.c0 + (w1 - w));
+    x.kh = x.u / p.units_per_kv;
+    x.row0 = (x.u - x.kh * p.units_per_kv) * NS * kTile;
+    x.nt = min(NS, (rows - x.row0 + kTile - 1) / kTile);
+    return x;
+  };
+
+  // Two tiles: 384 threads start with 168 registers each (64,512 in all); 224 for a softmax thread, which holds 128 scores,
+  // and 56 for the others are 2 x 128 x 224 + 128 x 56 = 64,512.
+  if (warp >= NS * 4) {
+    if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if (warp == kCopyWarp) {
+    if ((tid & 31) == 0) {
+      int st = 0;
+      uint32_t ph = 0;  // the first pass over the stages waits for nothing
+      int issued = 0;
+      bool ok = true;
+      for (long long w = w0; w < w1 && ok;) {
+        const Piece x = piece_at(w);
+        for (int c = x.c0; c < x.c1 && ok; ++c)
+          for (int kv = 0; kv < 2 && ok; ++kv) {
+            ok = wait(&empty[st], ph ^ 1, &s_fail);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&full[st], C::kTB);
+            for (int h = 0; h < HD / 64; ++h)
+              tma3(ring + st * C::kTB + h * kTile * 128, kv ? &maps.v : &maps.k, h * 64, c * kTile, x.kh, &full[st]);
+            ++issued;
+            if (++st == ST) { st = 0; ph ^= 1; }
+          }
+        w += x.c1 - x.c0;
+      }
+      if (!ok)  // the copies in flight land before the block leaves
+        for (int i = 0; i < ST && i < issued; ++i) {
+          const int at = issued - 1 - i;
+          mbar_wait_bounded(&full[at % ST], (at / ST) & 1);
+        }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    if ((tid & 31) == 0) {
+      uint32_t n_stage = 0;            // stages taken so far, K and V in turn
+      uint32_t ph_q[NS] = {}, ph_p[NS] = {}, ph_f[NS] = {};
+      bool ok = true;
+      constexpr uint32_t id_s = idesc(kTile, 0), id_o = idesc(HD, 1);
+      auto scores = [&](int i, uint32_t stage) {
+        uint64_t dk = tc::sdesc(tc::su32(ring + stage * C::kTB)), dq = tc::sdesc(tc::su32(sq + i * TERMS * C::kTB));
+        opaque(dk);  // descriptors are added up in place: hoisted out of the loop they would spill
+        opaque(dq);
+#pragma unroll
+        for (int e = TERMS - 1; e >= 0; --e)  // the small terms first
+#pragma unroll
+          for (int ks = 0; ks < HD / 16; ++ks) {
+            const int off = (ks >> 2) * kTile * 128 + (ks & 3) * 32;
+            tc::mma(tm + C::s_col(i), dq + ((e * C::kTB + off) >> 4), dk + (off >> 4), id_s, e < TERMS - 1 || ks > 0);
+          }
+        tc::commit(&s_full[i]);
+      };
+      for (long long w = w0; w < w1 && ok;) {
+        const Piece x = piece_at(w);
+        for (int i = 0; i < x.nt && ok; ++i) {
+          ok = wait(&q_ready[i], ph_q[i], &s_fail);
+          ph_q[i] ^= 1;
+        }
+        if (!ok) break;
+        tc::fence_after();
+        uint32_t kst = n_stage % ST;
+        ok = wait(&full[kst], (n_stage / ST) & 1, &s_fail);
+        if (!ok) break;
+        ++n_stage;
+        for (int i = 0; i < x.nt; ++i) scores(i, kst);
+        tc::commit(&empty[kst]);
+        for (int c = x.c0; c < x.c1 && ok; ++c) {
+          const uint32_t vst = n_stage % ST, vph = (n_stage / ST) & 1;
+          ++n_stage;
+          const bool more = c + 1 < x.c1;
+          const uint32_t k2 = n_stage % ST, kph = (n_stage / ST) & 1;
+          if (more) ++n_stage;
+          for (int i = 0; i < x.nt && ok; ++i) {
+            if (NS == 1 && more) {  // P does not lie over S: the next scores run during this chunk's softmax
+              ok = wait(&s_free[i], ph_f[i], &s_fail) && wait(&full[k2], kph, &s_fail);
+              ph_f[i] ^= 1;
+              if (!ok) break;
+              tc::fence_after();
+              scores(i, k2);
+              tc::commit(&empty[k2]);
+            }
+            ok = wait(&p_ready[i], ph_p[i], &s_fail);
+            ph_p[i] ^= 1;
+            if (ok && i == 0) ok = wait(&full[vst], vph, &s_fail);
+            if (!ok) break;
+            tc::fence_after();
+            uint64_t dv = desc_v(tc::su32(ring + vst * C::kTB));
+            opaque(dv);
+#pragma unroll
+            for (int e = TERMS - 1; e >= 0; --e)
+#pragma unroll
+              for (int ks = 0; ks < kTile / 16; ++ks)
+                mma_ts(tm + C::o_col(i), tm + C::p_col(i) + e * 64 + ks * 8, dv + ((ks * 2048) >> 4), id_o,
+                       c > x.c0 || e < TERMS - 1 || ks > 0);
+            if (i == x.nt - 1) tc::commit(&empty[vst]);
+            if (!more) tc::commit(&o_full[i]);
+            if (NS == 2 && more) {
+              if (i == 0) ok = wait(&full[k2], kph, &s_fail);
+              if (!ok) break;
+              scores(i, k2);  // after this tile's P V, which reads what it overwrites
+              if (i == x.nt - 1) tc::commit(&empty[k2]);
+            }
+            if (NS == 1 && more) tc::commit(&pv_done);
+          }
+        }
+        w += x.c1 - x.c0;
+      }
+      if (!ok) {  // the products in flight end before the block leaves
+        tc::commit(&drain);
+        mbar_wait_bounded(&drain, 0);
+      }
+    }
+    __syncwarp();
+  }
+  } else {
+    if (NS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int slot = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t to = tm + C::o_col(slot) + lanes, tp = tm + C::p_col(slot) + lanes;
+    uint32_t ph_s = 0, ph_o = 0, ph_v = 0;
+    bool ok = true;
+    for (long long w = w0; w < w1 && ok;) {
+      const Piece x = piece_at(w);
+      w += x.c1 - x.c0;
+      if (slot >= x.nt) continue;
+      const int row = x.row0 + slot * kTile + r;
+      const bool valid = row < rows;
+      {
+        const int b = row / p.gq, h = x.kh * p.gq + row % p.gq;
+        const long long at = ((long long)b * p.hq + h) * HD;
+        unsigned char* dst = sq + slot * TERMS * C::kTB;
+#pragma unroll 4
+        for (int e = 0; e < HD; e += 8) {
+          if (TERMS == 1) {
+            const uint4 v = valid ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at + e) : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(dst + swz(r, e)) = v;
+          } else {
+            float f[8] = {};
+            if (valid) {
+              const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at + e);
+              const float4 c = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at + e + 4);
+              f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = c.x; f[5] = c.y; f[6] = c.z; f[7] = c.w;
+            }
+#pragma unroll
+            for (int t = 0; t < TERMS; ++t) {
+              uint4 v;
+              v.x = take_pair(f[0], f[1]); v.y = take_pair(f[2], f[3]); v.z = take_pair(f[4], f[5]); v.w = take_pair(f[6], f[7]);
+              *reinterpret_cast<uint4*>(dst + t * C::kTB + swz(r, e)) = v;
+            }
+          }
+        }
+      }
+      tc::fence_async_smem();
+      mbar_arrive(&q_ready[slot]);
+      float m = -INFINITY, l = 0.f;
+      for (int c = x.c0; c < x.c1; ++c) {
+        ok = wait(&s_full[slot], ph_s, &s_fail);
+        ph_s ^= 1;
+        if (!ok) break;
+        tc::fence_after();
+        float sv[kTile];
+#pragma unroll
+        for (int j = 0; j < kTile; j += 32) tc::load_rows(tm + C::s_col(slot) + j, warp, reinterpret_cast<uint32_t*>(sv + j));
+        if (NS == 1 && c + 1 < x.c1) {
+          tc::fence_before();
+          mbar_arrive(&s_free[slot]);
+        }
+        const int left = p.P - c * kTile;  // keys of this chunk
+        if (left < kTile) {
+#pragma unroll
+          for (int j = 0; j < kTile; ++j)
+            if (j >= left) sv[j] = -INFINITY;
+        }
+        float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+        for (int j = 4; j < kTile; ++j) mx[j & 3] = fmaxf(mx[j & 3], sv[j]);
+        const float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        const bool grow = c == x.c0 || mc > m + 8.f;
+        float al = 1.f;
+        if (grow) {
+          const float mn = fmaxf(m, mc);
+          al = mn == -INFINITY ? 1.f : ex2(m - mn);
+          m = mn;
+          l *= al;
+        }
+        if (NS == 1 && c > x.c0) {  // P and O are this thread's once the last P V is done
+          ok = wait(&pv_done, ph_v, &s_fail);
+          ph_v ^= 1;
+          if (!ok) break;
+          tc::fence_after();
+        }
+        // with two tiles every P V so far is done: the scores just read were issued after it
+        if (c > x.c0 && __any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int j = 0; j < HD; j += 16) {
+            uint32_t ov[16];
+            tc::load_rows16(tm + C::o_col(slot) + j, warp, ov);
+#pragma unroll
+            for (int t = 0; t < 16; ++t) ov[t] = __float_as_uint(__uint_as_float(ov[t]) * al);
+            tm_st16(to + j, ov);
+          }
+          tm_st_wait();
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < kTile; j += 64) {
+#pragma unroll
+          for (int t = 0; t < 64; ++t) {
+            sv[j + t] = ex2(fmaf(sv[j + t], p.scale_log2, -mu));
+            ls[t & 3] += sv[j + t];
+          }
+#pragma unroll
+          for (int e = 0; e < TERMS; ++e) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int t = 0; t < 32; ++t) pk[t] = take_pair(sv[j + 2 * t], sv[j + 2 * t + 1]);
+            tm_st32(tp + e * 64 + j / 2, pk);
+          }
+        }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        tm_st_wait();
+        tc::fence_before();
+        mbar_arrive(&p_ready[slot]);
+      }
+      if (!ok) break;
+      ok = wait(&o_full[slot], ph_o, &s_fail);
+      ph_o ^= 1;
+      if (!ok) break;
+      tc::fence_after();
+      // unnormalised O and (m, l) of the row
+      const long long part_row = (long long)(blockIdx.x + x.u) * (NS * kTile) + slot * kTile + r;
+      float* po = p.part + part_row * HD;
+#pragma unroll
+      for (int j = 0; j < HD; j += 32) {
+        uint32_t ov[32];
+        tc::load_rows(tm + C::o_col(slot) + j, warp, ov);
+        if (valid)
+#pragma unroll
+          for (int t = 0; t < 32; t += 4) *reinterpret_cast<uint4*>(po + j + t) = make_uint4(ov[t], ov[t + 1], ov[t + 2], ov[t + 3]);
+      }
+      p.part_ml[part_row] = make_float2(m, l);
+    }
+    if (!ok)  // a wait gave up: the rows of this block's pieces come out NaN
+      for (long long w = w0; w < w1;) {
+        const Piece x = piece_at(w);
+        w += x.c1 - x.c0;
+        p.part_ml[(long long)(blockIdx.x + x.u) * (NS * kTile) + slot * kTile + r] = make_float2(0.f, NAN);
+      }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) tc::free_cols(tm, 512);
+}
+
 
 template <int HD, int TERMS>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ Params p) {
@@ -98,13 +508,14 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
   for (int e = 0; e < HD / 16; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // heads 2 t, 2 t + 1
 
-  const int nkeys = bad ? 0 : p.P + len;
+  const int P = p.use_prefix ? 0 : p.P;  // prefix keys that this kernel reads itself
+  const int nkeys = bad ? 0 : P + len;
   for (int key0 = warp * 16; key0 < nkeys; key0 += kWarps * 16) {
     // keys of this lane: as rows g, g + 8 of K and as 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of V
     auto row = [&](const __nv_bfloat16* pre, const __nv_bfloat16* own, int key) {
       key = min(key, nkeys - 1);
-      return key < p.P ? pre + ((long long)kh * p.prefix_cap + key) * HD
-                       : own + (((long long)b * p.hkv + kh) * p.max_seq + (key - p.P)) * HD;
+      return key < P ? pre + ((long long)kh * p.prefix_cap + key) * HD
+                     : own + (((long long)b * p.hkv + kh) * p.max_seq + (key - P)) * HD;
     };
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     const __nv_bfloat16 *ka = row(p.pk, p.kc, key0 + g) + 8 * t, *kb = row(p.pk, p.kc, key0 + g + 8) + 8 * t;
@@ -186,10 +597,23 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
     d0[lo] = o[e][0]; d0[HD + lo] = o[e][1]; d0[hi] = o[e][2]; d0[HD + hi] = o[e][3];
   }
   __syncthreads();
+  pdl_wait();  // the prefix kernel's parts are there (every block waits, so that this grid ends after that one)
+  constexpr int NS = Cfg<HD, TERMS>::kSlots;
+  const bool none = p.P == 0 && len == 0;
   for (int i = tid; i < nh * HD; i += kThreads) {
     const int h = i / HD, d = i % HD;
+    // the parts of this row: slots first + u .. last + u of its unit
+    const int row = b * p.gq + hb * kHeads + h, u = kh * p.units_per_kv + row / (NS * kTile);
+    int first = 0, last = -1;
+    if (p.use_prefix) {
+      const long long total = (long long)p.units * p.nch;
+      first = (int)((((long long)u * p.nch + 1) * p.n_cta - 1) / total);
+      last = (int)(((long long)(u + 1) * p.nch * p.n_cta - 1) / total);
+    }
+    const long long at0 = (long long)(first + u) * (NS * kTile) + row % (NS * kTile);
     float mx = -INFINITY;
     for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][h]);
+    for (int j = 0; j <= last - first; ++j) mx = fmaxf(mx, __ldcg(&p.part_ml[at0 + (long long)j * NS * kTile]).x);
     const float mu = mx == -INFINITY ? 0.f : mx;
     float lt = 0.f, ot = 0.f;
     for (int w = 0; w < kWarps; ++w) {
@@ -197,19 +621,101 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
       lt += s_l[w][h] * a;
       ot += s_o[(w * kHeads + h) * HD + d] * a;
     }
-    float y = bad ? NAN : nkeys == 0 ? 0.f : ot / lt;
+#pragma unroll 4
+    for (int j = 0; j <= last - first; ++j) {
+      const long long at = at0 + (long long)j * NS * kTile;
+      const float2 ml = __ldcg(&p.part_ml[at]);
+      const float a = ex2(ml.x - mu);
+      lt += ml.y * a;
+      ot += __ldcg(&p.part[at * HD + d]) * a;
+    }
+    const float y = bad ? NAN : none ? 0.f : ot / lt;
     const long long at = ((long long)b * p.hq + h0 + h) * HD + d;
     if (TERMS > 1) static_cast<float*>(p.out)[at] = y;
     else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
-    if (d == 0 && p.lse) p.lse[(long long)b * p.hq + h0 + h] = bad ? NAN : nkeys == 0 ? -INFINITY : mx * kLn2 + logf(lt);
+    if (d == 0 && p.lse) p.lse[(long long)b * p.hq + h0 + h] = bad ? NAN : none ? -INFINITY : mx * kLn2 + logf(lt);
   }
 }
 
+// Prefix keys through the tensor cores, or read by the rows kernel of every sequence.
+bool prefix_pays(int B, int hkv, int hd, int P) {
+  (void)B; (void)hkv; (void)hd;
+  return P > 0;
+}
+
+// Units, runs and chunks of the prefix kernel; `ns` row tiles a unit.
+void prefix_geometry(int rows, int hkv, int P, int ns, int sms, Params* p) {
+  p->units_per_kv = (rows + ns * kTile - 1) / (ns * kTile);
+  p->units = hkv * p->units_per_kv;
+  p->nch = (P + kTile - 1) / kTile;
+  const long long total = (long long)p->units * p->nch;
+  p->n_cta = (int)(total < sms ? total : sms);
+}
+size_t part_rows(const Params& p, int ns) { return ((size_t)p.n_cta + p.units) * ns * kTile; }
+
+cudaError_t encode_map(CUtensorMap* out, const void* base, int hd, int P, int cap, int hkv) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  static std::mutex mu;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!encode) {
+      void* fn = nullptr;
+      cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+      const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+      if (e != cudaSuccess) return e;
+      if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
+  }
+  // (element, key, kv head); the key dimension ends at P: keys beyond it are zeros in shared memory
+  const cuuint64_t dim[3] = {(cuuint64_t)hd, (cuuint64_t)P, (cuuint64_t)hkv};
+  const cuuint64_t stride[2] = {(cuuint64_t)hd * 2, (cuuint64_t)cap * hd * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)kTile, 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dim, stride, box, one,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <int HD, int TERMS>
-cudaError_t launch_rows(const Params& p, cudaStream_t s) {
-  const size_t smem = (size_t)kWarps * kHeads * HD * 4;
-  rows_kernel<HD, TERMS><<<(unsigned)(p.B * p.hkv * p.hblocks), kThreads, smem, s>>>(p);
-  return cudaGetLastError();
+cudaError_t launch(Params& p, void* workspace, cudaStream_t s) {
+  using C = Cfg<HD, TERMS>;
+  if (p.use_prefix) {
+    prefix_geometry(p.B * p.gq, p.hkv, p.P, C::kSlots, num_sms(), &p);
+    p.part = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(p.part + part_rows(p, C::kSlots) * HD);
+    PrefixMaps maps;
+    cudaError_t e = encode_map(&maps.k, p.pk, HD, p.P, (int)p.prefix_cap, p.hkv);
+    if (e == cudaSuccess) e = encode_map(&maps.v, p.pv, HD, p.P, (int)p.prefix_cap, p.hkv);
+    if (e != cudaSuccess) return e;
+    static std::mutex mu;
+    static bool set[64] = {};  // the shared-memory limit belongs to a device
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    {
+      std::lock_guard<std::mutex> lock(mu);
+      if (dev >= 64 || !set[dev]) {
+        e = cudaFuncSetAttribute(prefix_kernel<HD, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) set[dev] = true;
+      }
+    }
+    prefix_kernel<HD, TERMS><<<p.n_cta, C::kThreads, C::kSmem, s>>>(p, maps);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)(p.B * p.hkv * p.hblocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)kWarps * kHeads * HD * 4;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.use_prefix ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, rows_kernel<HD, TERMS>, p);
 }
 
 bool sizes_ok(int B, int hq, int hkv, int hd, int P) {
@@ -224,7 +730,15 @@ using namespace spd;
 extern "C" size_t spd_shared_prefix_attention_workspace_bytes(int32_t B, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
                                                               int32_t prefix_len) {
   if (!spa::sizes_ok(B, n_heads, n_kv_heads, head_dim, prefix_len)) return 0;
-  return 16;
+  if (!spa::prefix_pays(B, n_kv_heads, head_dim, prefix_len)) return 16;
+  size_t rows = 0;
+  for (int ns = 1; ns <= 2; ++ns) {  // tiles a unit: fp32 and bf16 queries
+    spa::Params p;
+    spa::prefix_geometry(B * (n_heads / n_kv_heads), n_kv_heads, prefix_len, ns, num_sms(), &p);
+    const size_t n = spa::part_rows(p, ns);
+    rows = n > rows ? n : rows;
+  }
+  return rows * (head_dim * sizeof(float) + sizeof(float2));
 }
 
 extern "C" int spd_shared_prefix_attention(const void* q, int32_t q_dtype, const void* prefix_k, const void* prefix_v,
@@ -250,16 +764,17 @@ extern "C" int spd_shared_prefix_attention(const void* q, int32_t q_dtype, const
   p.q = q;
   p.pk = static_cast<const __nv_bfloat16*>(prefix_k); p.pv = static_cast<const __nv_bfloat16*>(prefix_v);
   p.kc = static_cast<const __nv_bfloat16*>(k_cache); p.vc = static_cast<const __nv_bfloat16*>(v_cache);
-  p.lens = lens; p.out = out; p.lse = lse; p.part = static_cast<float*>(workspace);
+  p.lens = lens; p.out = out; p.lse = lse;
   p.prefix_cap = prefix_cap; p.max_seq = max_seq; p.P = prefix_len; p.B = B; p.hq = n_heads; p.hkv = n_kv_heads;
   p.gq = n_heads / n_kv_heads;
   p.hblocks = (p.gq + spa::kHeads - 1) / spa::kHeads;
   p.scale_log2 = spa::kLog2e / std::sqrt((float)head_dim);
+  p.use_prefix = spa::prefix_pays(B, n_kv_heads, head_dim, prefix_len);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(cuda_stream);
   cudaGetLastError();
   cudaError_t e;
-  if (head_dim == 128) e = q_dtype == SPD_DTYPE_F32 ? spa::launch_rows<128, 3>(p, s) : spa::launch_rows<128, 1>(p, s);
-  else e = q_dtype == SPD_DTYPE_F32 ? spa::launch_rows<64, 3>(p, s) : spa::launch_rows<64, 1>(p, s);
+  if (head_dim == 128) e = q_dtype == SPD_DTYPE_F32 ? spa::launch<128, 3>(p, workspace, s) : spa::launch<128, 1>(p, workspace, s);
+  else e = q_dtype == SPD_DTYPE_F32 ? spa::launch<64, 3>(p, workspace, s) : spa::launch<64, 1>(p, workspace, s);
   if (e != cudaSuccess) {
     char msg[160];
     snprintf(msg, sizeof(msg), "spd_shared_prefix_attention: launch: %s", cudaGetErrorString(e));
