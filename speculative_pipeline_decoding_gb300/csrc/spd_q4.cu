@@ -8,11 +8,13 @@
 //
 // Packed layout: one record for each 16 rows (tile) and 128 columns (block), records of a tile in a row:
 //   1024 B codes   [h 0..1][lane 0..31][word 0..3]: word w of lane (g = lane / 4, t = lane % 4) holds the 8 codes of
-//                  row g + 8 h, columns 32 w + 8 t .. + 7, lowest column in the lowest bits
-//   scales         [128 / group][16 rows], scale_dtype
-//   zeros          [128 / group][16 rows] bf16 of 128 + zero (only with zeros)
-// so that a warp reads a record in two 16-byte loads a lane, already in the order of the mma's A operand: the four bf16
-// pairs of a word are (code i, code i + 4), i = 0..3, taken as (w >> 4 i) & 0x000f000f | 0x43004300 = 128 + code.  Columns
+//                  row g + 8 h, columns 32 w + 8 t .. + 7: column 2 i in nibble i, column 2 i + 1 in nibble i + 4, the
+//                  word rotated left by 3
+//   scales         [row g of 8][h][128 / group], scale_dtype: a lane's scales are neighbours
+//   zeros          the same order, bf16 of -(16 + zero) (only with zeros)
+// so that a warp reads a record in two 16-byte loads a lane (and one or two for scales and zeros), already in the order of the mma's A operand: the four bf16
+// pairs of a word are columns (2 i, 2 i + 1), i = 0..3, taken as rotr(w, 4 i) & 0x00780078 | 0x41804180 = 16 + code: the
+// code in the upper mantissa bits of 16.0, exact; 16 + zero is then taken off, exact as well.  Columns
 // beyond `cols` and rows beyond `rows` hold code = zero and scale 0.
 #include <cmath>
 #include <cstdio>
@@ -24,7 +26,7 @@
 namespace spd {
 namespace q4 {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCols = 32768;
 constexpr int kMaxM = 32;
@@ -90,22 +92,24 @@ __global__ void pack_kernel(const uint8_t* codes, const void* scales, const uint
     uint32_t w[4];
     for (int i = 0; i < 4; ++i) {
       const int c = kb * 128 + 32 * i + 8 * (lane & 3);
-      w[i] = 0x88888888u;
+      w[i] = 0x44444444u;  // 8 in every nibble
       if (r < rows && c < cols) {  // whole words: cols is a multiple of 32
         const uint8_t* src = codes + (long long)r * (cols >> 1) + (c >> 1);
-        w[i] = (uint32_t)src[0] | (uint32_t)src[1] << 8 | (uint32_t)src[2] << 16 | (uint32_t)src[3] << 24;
+        w[i] = 0;
+        for (int b = 0; b < 4; ++b) w[i] |= (uint32_t)(src[b] & 15) << (4 * b) | (uint32_t)(src[b] >> 4) << (4 * b + 16);
+        w[i] = w[i] << 3 | w[i] >> 29;
       }
     }
     *reinterpret_cast<uint4*>(out + h * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  for (int i = lane; i < ng * 16; i += 32) {
-    const int r = tile * 16 + (i & 15), gc = kb * ng + (i >> 4);
+  for (int i = lane; i < ng * 16; i += 32) {  // (g, h, group of the block)
+    const int r = tile * 16 + i / (2 * ng) + 8 * (i / ng % 2), gc = kb * ng + i % ng;
     const bool in = r < rows && gc < per_row;
     const long long at = (long long)r * per_row + gc;
     if (s_f32) reinterpret_cast<float*>(out + 1024)[i] = in ? static_cast<const float*>(scales)[at] : 0.f;
     else reinterpret_cast<__nv_bfloat16*>(out + 1024)[i] = in ? static_cast<const __nv_bfloat16*>(scales)[at] : __nv_bfloat16(0.f);
     if (zeros)
-      reinterpret_cast<__nv_bfloat16*>(out + 1024 + ng * 16 * (s_f32 ? 4 : 2))[i] = __float2bfloat16_rn(128.f + (in ? zeros[at] : 8));
+      reinterpret_cast<__nv_bfloat16*>(out + 1024 + ng * 16 * (s_f32 ? 4 : 2))[i] = __float2bfloat16_rn(-16.f - (in ? zeros[at] : 8));
   }
 }
 
@@ -118,172 +122,403 @@ struct Group {
   void* y;
   long long xs, ys;
   int rows, tile0;  // first tile of the group
+  int vec, pad;     // x's rows start on 16 bytes
 };
 struct Params {
   Group g[kMaxExplicit];
   int G, M, cols, nkb, tiles;
-  int gw;            // 32-column words of a group: 1, 2 or 4
   int rec, s_f32, has_z, x_f32;
   int terms, mb;     // bf16 terms of a vector, vectors of a block
+  int chunk, batch;  // column blocks of the vectors in shared memory at a time; tiles between two meetings of the warps
   const float* nw;
+  int nvec;          // nw starts on 16 bytes
   float eps;
 };
 
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// pair i of a word, less its zero point: (code i - z, code i + 4 - z) in bf16, exact
-__device__ __forceinline__ uint32_t pair(uint32_t w, int i, __nv_bfloat162 z) {
-  uint32_t u = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-  __nv_bfloat162 v = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&u), z);
-  return *reinterpret_cast<uint32_t*>(&v);
+// the same with a zero sum to start from
+__device__ __forceinline__ void mma16816_first(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
-// the next bf16 term of v by truncation (no overflow to infinity); v keeps the rest
-__device__ __forceinline__ uint32_t take_term(float& v) {
-  const uint32_t u = (__float_as_uint(v) & 0xffff0000u) | (v != v ? 0x400000u : 0u);  // a NaN stays one
-  const float h = __uint_as_float(u);
-  v = fabsf(h) == INFINITY ? 0.f : v - h;  // an infinity's rest is not NaN
-  return u >> 16;
+// pair i of a word as (16 + code, 16 + code) in bf16: (w & mask) | magic in one instruction, the magic number in a register
+__device__ __forceinline__ uint32_t pair(uint32_t w, int i, uint32_t magic) {
+  uint32_t u;
+  asm("lop3.b32 %0, %1, 0x00780078, %2, 0xea;" : "=r"(u) : "r"(__funnelshift_r(w, w, 4 * i)), "r"(magic));
+  return u;
+}
+__device__ __forceinline__ uint32_t add2(uint32_t u, uint32_t z) {
+  const __nv_bfloat162 v = __hadd2(*reinterpret_cast<__nv_bfloat162*>(&u), *reinterpret_cast<__nv_bfloat162*>(&z));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Eight consecutive columns of a vector as `terms` bf16 terms, 16 bytes each, `step` apart.  A term is the value's upper
+// half (truncated: no overflow to infinity), the rest goes on to the next; the last of two is rounded to nearest.
+__device__ __forceinline__ void split8(float* v, int terms, uint4* dst, int step) {
+  float f = 0.f;  // 0 if all are finite, else NaN
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f = fmaf(v[j], 0.f, f);
+  for (int e = 0; e < terms; ++e, dst += step) {
+    uint32_t o[4];
+    if (f == 0.f) {
+      if (e == 1 && terms == 2) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+          o[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = __byte_perm(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]), 0x7632);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] -= __uint_as_float(__float_as_uint(v[j]) & 0xffff0000u);
+      }
+    } else {
+      // infinities and NaN stay what they are in the first term; a NaN keeps a bit in its upper half
+      uint32_t h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        h[j] = (__float_as_uint(v[j]) | (v[j] != v[j] ? 0x400000u : 0u)) & 0xffff0000u;
+        v[j] = fabsf(v[j]) < INFINITY ? v[j] - __uint_as_float(h[j]) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = h[2 * j] >> 16 | h[2 * j + 1];
+    }
+    *dst = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+// Bytes of dynamic shared memory: vectors of a chunk and 64 zero bytes, parts of the warps, sums over the chunks so far.
+struct Smem {
+  uint32_t part, sums, total;
+};
+__host__ __device__ inline Smem smem_of(int chunk, int nkb, int ncol, int nt, int batch, int mb) {
+  Smem s;
+  s.part = (uint32_t)chunk * 4 * ncol * 64 + 64;
+  s.sums = s.part + (uint32_t)(batch + kWarps - 1) * 16 * (nt * 8 + 1) * 4;
+  s.total = s.sums + (chunk < nkb ? (uint32_t)16 * batch * mb * 4 : 0);
+  return s;
 }
 
-// Block: 8 warps share a tile of 16 rows, each taking a run of its 128-column blocks; sums of the warps meet in shared
-// memory.  Blocks are persistent over tiles; the vectors are split into terms once per block, into shared memory as
-// [column block][word][operand column][t] of 16 bytes (two mma steps of a lane).
-template <int NT>
-__global__ void __launch_bounds__(kThreads) gemv_kernel(const __grid_constant__ Params p) {
-  extern __shared__ __align__(16) unsigned char smem[];
+__device__ __forceinline__ uint4 ld16(const unsigned char* p) {  // read once: not kept in L1
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+template <int N>
+__device__ __forceinline__ void ld_words(const unsigned char* p, uint32_t* w) {
+  if (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+    }
+  } else if (N == 2) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    w[0] = __ldg(reinterpret_cast<const unsigned*>(p));
+  }
+}
+
+// A lane's share of a record, on its way from memory.
+template <int NG> struct Record {
+  uint4 a0, a1;
+  uint32_t s[2 * NG], z[NG];  // fp32 scales, or bf16 ones in the first half; zeros
+};
+
+// A block owns a run of tiles and takes them in batches.  The records of a batch are dealt to its 8 warps in equal runs,
+// whatever tiles they fall into: a warp reads its run as one stream, kAhead records ahead in registers, and leaves the sum of
+// each tile it touched in shared memory, as part warp + tile.  The warps meet once a batch, to add the parts up in their
+// order.  The vectors are split into terms once per block, as [column block][word][operand column][t] of 16 bytes (two mma
+// steps of a lane); where they do not fit at once the columns are taken in chunks, sums over the chunks in shared memory.
+// The limit besides memory is the instruction rate: about 11 instructions a word of 8 codes, 88 of some 130 a record.
+template <int NT, int GW>  // operand tiles; 32-column words of a group (1, 2, 4)
+__global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int NG = 4 / GW, PC = NT * 8 + 1;
+  constexpr int kChains = NT == 2 ? 2 : 1;
+  constexpr int kAhead = NT == 1 ? 4 : NT == 2 ? (NG < 4 ? 4 : 3) : 2;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g4 = lane >> 2, t4 = lane & 3;
   const int m0 = blockIdx.y * p.mb, mb = min(p.mb, p.M - m0), ncol = mb * p.terms;
+  const int nc = gridDim.x, cid = blockIdx.x;
+  const int first = cid * (p.tiles / nc) + min(cid, p.tiles % nc), last = first + p.tiles / nc + (cid < p.tiles % nc);
+  const Smem L = smem_of(p.chunk, p.nkb, p.mb * p.terms, NT, p.batch, p.mb);
   uint4* xs = reinterpret_cast<uint4*>(smem);
-  float* part = reinterpret_cast<float*>(smem + (size_t)p.nkb * 4 * p.mb * p.terms * 64);  // [2][warp][16][NT * 8 + 1]
-  __shared__ float s_ss[kMaxM];
-  constexpr int PC = NT * 8 + 1;
-  const int kb0 = warp * p.nkb / kWarps, kb1 = (warp + 1) * p.nkb / kWarps;
+  float* part = reinterpret_cast<float*>(smem + L.part);  // [batch + 7][16][NT * 8 + 1]
+  float* sums = reinterpret_cast<float*>(smem + L.sums);  // [mb][16 * batch]
+  __shared__ float s_ss[kWarps][kMaxM], s_sum[kMaxM];
+  if (tid < 4) reinterpret_cast<uint4*>(smem + L.part - 64)[tid] = make_uint4(0, 0, 0, 0);
+  // this lane's column of each operand tile; columns that do not exist read the zero bytes, at a step of 0
+  uint32_t x0[NT], xstep[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const bool in = n * 8 + g4 < ncol;
+    x0[n] = in ? ((n * 8 + g4) * 4 + t4) * 16 : L.part - 64 + t4 * 16;
+    xstep[n] = in ? ncol * 64 : 0;
+  }
+  uint32_t magic;
+  asm volatile("mov.b32 %0, 0x41804180;" : "=r"(magic));
+  const uint32_t soff = 1024 + g4 * (2 * NG) * (p.s_f32 ? 4 : 2), zoff = 1024 + 16 * NG * (p.s_f32 ? 4 : 2) + g4 * (2 * NG) * 2;
+  auto load = [&](Record<NG>& r, const unsigned char* src) {
+    r.a0 = ld16(src + lane * 16);
+    r.a1 = ld16(src + 512 + lane * 16);
+    if (p.s_f32) ld_words<2 * NG>(src + soff, r.s);
+    else ld_words<NG>(src + soff, r.s);
+    if (p.has_z) ld_words<NG>(src + zoff, r.z);
+  };
+  pdl_wait();
+  pdl_trigger();
   const void* staged = nullptr;
-  int parity = 0;
-  for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, parity ^= 1) {
-    int gi = 0;
-    while (gi + 1 < p.G && tile >= p.g[gi + 1].tile0) ++gi;
+  int staged_kb = -1;
+  for (int t0 = first, t1; t0 < last; t0 = t1) {
+    int gi = 0;  // a batch is of one matrix
+    while (gi + 1 < p.G && t0 >= p.g[gi + 1].tile0) ++gi;
     const Group& G = p.g[gi];
-    if (G.x != staged) {
-      __syncthreads();
-      if (tid < kMaxM) s_ss[tid] = 0.f;
-      __syncthreads();
-      // 8 consecutive columns of one vector a thread
-      const int per = p.nkb * 16;
-      for (int m = warp; m < mb; m += kWarps) {
-        float ss = 0.f;
-        for (int i = lane; i < per; i += 32) {
-          const int c = i * 8;
-          float v[8];
-          for (int j = 0; j < 8; ++j) v[j] = 0.f;
-          if (c < p.cols) {
-            const long long at = (long long)(m0 + m) * G.xs + c;
-            for (int j = 0; j < 8; ++j)
-              v[j] = p.x_f32 ? static_cast<const float*>(G.x)[at + j] : __bfloat162float(static_cast<const __nv_bfloat16*>(G.x)[at + j]);
-            if (p.nw)
-              for (int j = 0; j < 8; ++j) {
-                ss += v[j] * v[j];
-                v[j] *= p.nw[c + j];
-              }
-          }
-          for (int e = 0; e < p.terms; ++e) {
-            uint32_t b[8];
-            for (int j = 0; j < 8; ++j) b[j] = take_term(v[j]);
-            // columns 8 i .. = block i / 16, word (i % 16) / 4, t = i % 4; pairs (j, j + 4)
-            xs[((i >> 2) * ncol + m * p.terms + e) * 4 + (i & 3)] =
-                make_uint4(b[0] | b[4] << 16, b[1] | b[5] << 16, b[2] | b[6] << 16, b[3] | b[7] << 16);
-          }
+    t1 = min(last, t0 + p.batch);
+    if (gi + 1 < p.G) t1 = min(t1, p.g[gi + 1].tile0);
+    const int nrow = 16 * (t1 - t0);
+    for (int kb_lo = 0; kb_lo < p.nkb; kb_lo += p.chunk) {
+      const int nk = min(p.chunk, p.nkb - kb_lo);
+      const int nrec = (t1 - t0) * nk, r0 = warp * nrec / kWarps, r1 = (warp + 1) * nrec / kWarps;
+      int u = r0 / nk, kb = r0 - u * nk;
+      const unsigned char* src = G.w + ((size_t)(t0 - G.tile0 + u) * p.nkb + kb_lo + kb) * p.rec;
+      int skb = kb;  // the column block that src stands at
+      auto advance = [&]() {
+        src += p.rec;
+        if (nk < p.nkb && ++skb == nk) {  // else tiles follow one another without a gap
+          skb = 0;
+          src += (size_t)(p.nkb - nk) * p.rec;
         }
-        if (p.nw) {
-          for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          if (lane == 0) s_ss[m] = rsqrtf(ss / p.cols + p.eps);
-        }
+      };
+      {  // the start of the run on its way to L2 while the vectors are split
+        const uint32_t bytes = (uint32_t)min(r1 - r0, nk < p.nkb ? nk - kb : 8) * p.rec;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if ((j * 32 + lane) * 128u < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + (j * 32 + lane) * 128));
       }
-      __syncthreads();
-      staged = G.x;
-    }
-    float tot[NT][4], acc[NT][4];
+      if (G.x != staged || kb_lo != staged_kb) {
+        // A warp takes 32 times 8 consecutive columns of a vector at a time, two such segments together; the last readers of
+        // the vectors are behind the barrier at the end of the chunk.
+        const int per = nk * 16, c0 = kb_lo * 128, segs = (per + 31) >> 5, nseg = segs * mb;
+        if (p.nw && lane < mb) s_ss[warp][lane] = 0.f;
+        __syncwarp();
+        if (p.terms == 1 && G.vec) {  // bf16 as it is
+          for (int q = warp; q < nseg; q += kWarps) {
+            const int m = q / segs, i = (q - m * segs) * 32 + lane;
+            if (i >= per) continue;
+            uint4* dst = xs + ((i >> 2) * ncol + m) * 4 + (i & 3);
+            if (c0 + i * 8 < p.cols)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
+                           "l"(static_cast<const __nv_bfloat16*>(G.x) + (long long)(m0 + m) * G.xs + c0 + i * 8)
+                           : "memory");
+            else
+              *dst = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("cp.async.commit_group;\n cp.async.wait_group 0;" ::: "memory");
+        } else {
+          constexpr int kU = 2;
+          for (int q0 = warp; q0 < nseg; q0 += kWarps * kU) {
+            float v[kU][8], nw[kU][8];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+            for (int k = 0; k < kU; ++k) {
+              const int q = q0 + k * kWarps, m = q / segs, i = (q - m * segs) * 32 + lane, c = c0 + i * 8;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tot[n][i] = acc[n][i] = 0.f;
-    const unsigned char* base = G.w + (size_t)(tile - G.tile0) * p.nkb * p.rec;
-    const int ng = 4 / p.gw, soff = 1024, zoff = 1024 + ng * 16 * (p.s_f32 ? 4 : 2);
-    for (int kb = kb0; kb < kb1; ++kb) {
-      const unsigned char* r = base + (size_t)kb * p.rec;
-      const uint4 a0 = __ldcs(reinterpret_cast<const uint4*>(r) + lane), a1 = __ldcs(reinterpret_cast<const uint4*>(r + 512) + lane);
-      const uint32_t w0[4] = {a0.x, a0.y, a0.z, a0.w}, w1[4] = {a1.x, a1.y, a1.z, a1.w};
-      __nv_bfloat162 z0 = __float2bfloat162_rn(136.f), z1 = z0;
+              for (int j = 0; j < 8; ++j) v[k][j] = 0.f;
+              if (q >= nseg || i >= per || c >= p.cols) continue;
+              const long long at = (long long)(m0 + m) * G.xs + c;
+              if (p.nw) {
+                if (p.nvec) {
+                  const float4 a = __ldg(reinterpret_cast<const float4*>(p.nw + c)), b = __ldg(reinterpret_cast<const float4*>(p.nw + c + 4));
+                  nw[k][0] = a.x; nw[k][1] = a.y; nw[k][2] = a.z; nw[k][3] = a.w; nw[k][4] = b.x; nw[k][5] = b.y; nw[k][6] = b.z; nw[k][7] = b.w;
+                } else {
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const int gr = w / p.gw;
-        if (p.has_z && w % p.gw == 0) {
-          const __nv_bfloat16* z = reinterpret_cast<const __nv_bfloat16*>(r + zoff) + gr * 16;
-          z0 = __bfloat162bfloat162(z[g4]);
-          z1 = __bfloat162bfloat162(z[g4 + 8]);
+                  for (int j = 0; j < 8; ++j) nw[k][j] = __ldg(p.nw + c + j);
+                }
+              }
+              if (p.x_f32) {
+                const float* x = static_cast<const float*>(G.x) + at;
+                if (G.vec) {
+                  const float4 a = *reinterpret_cast<const float4*>(x), b = *reinterpret_cast<const float4*>(x + 4);
+                  v[k][0] = a.x; v[k][1] = a.y; v[k][2] = a.z; v[k][3] = a.w; v[k][4] = b.x; v[k][5] = b.y; v[k][6] = b.z; v[k][7] = b.w;
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) v[k][j] = x[j];
+                }
+              } else {
+                const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(G.x) + at;
+                if (G.vec) {
+                  const uint4 w = *reinterpret_cast<const uint4*>(x);
+                  WTraits<__nv_bfloat16>::unpack(w, v[k]);
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) v[k][j] = __bfloat162float(x[j]);
+                }
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < kU; ++k) {
+              const int q = q0 + k * kWarps, m = q / segs, i = (q - m * segs) * 32 + lane, c = c0 + i * 8;
+              if (q >= nseg) continue;  // the whole warp
+              if (p.nw) {
+                float ss = 0.f;
+                if (i < per && c < p.cols) {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) {
+                    ss += v[k][j] * v[k][j];
+                    v[k][j] *= nw[k][j];
+                  }
+                }
+#pragma unroll
+                for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                if (lane == 0) s_ss[warp][m] += ss;
+              }
+              // block i / 16, word (i % 16) / 4, t = i % 4
+              if (i < per) split8(v[k], p.terms, xs + ((i >> 2) * ncol + m * p.terms) * 4 + (i & 3), 4);
+            }
+          }
         }
-        uint4 b[NT];
+        __syncthreads();
+        if (p.nw && tid < mb) {
+          float ss = kb_lo ? s_sum[tid] : 0.f;
+          for (int w = 0; w < kWarps; ++w) ss += s_ss[w][tid];
+          s_sum[tid] = ss;  // read behind the barrier of the parts
+        }
+        staged = G.x;
+        staged_kb = kb_lo;
+      }
+      Record<NG> rec[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (r0 + j < r1) {
+          load(rec[j], src);
+          advance();
+        }
+      float tot[NT][4], acc[NT][kChains][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) tot[n][0] = tot[n][1] = tot[n][2] = tot[n][3] = 0.f;
+      auto flush = [&]() {
+        float* mine = part + (warp + u) * 16 * PC + g4 * PC + 2 * t4;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const int col = n * 8 + g4;
-          b[n] = col < ncol ? xs[((kb * 4 + w) * ncol + col) * 4 + t4] : make_uint4(0, 0, 0, 0);
+          mine[n * 8] = tot[n][0];
+          mine[n * 8 + 1] = tot[n][1];
+          mine[8 * PC + n * 8] = tot[n][2];
+          mine[8 * PC + n * 8 + 1] = tot[n][3];
+          tot[n][0] = tot[n][1] = tot[n][2] = tot[n][3] = 0.f;
         }
-        uint32_t a[4];
-        a[0] = pair(w0[w], 0, z0); a[1] = pair(w1[w], 0, z1); a[2] = pair(w0[w], 1, z0); a[3] = pair(w1[w], 1, z1);
+      };
+      for (int at = r0; at < r1; at += kAhead) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816(acc[n], a, b[n].x, b[n].y);
-        a[0] = pair(w0[w], 2, z0); a[1] = pair(w1[w], 2, z1); a[2] = pair(w0[w], 3, z0); a[3] = pair(w1[w], 3, z1);
+        for (int j = 0; j < kAhead; ++j) {
+          if (at + j >= r1) break;
+          const Record<NG>& r = rec[j];
+          const uint32_t w0[4] = {r.a0.x, r.a0.y, r.a0.z, r.a0.w}, w1[4] = {r.a1.x, r.a1.y, r.a1.z, r.a1.w};
+          uint32_t xk[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816(acc[n], a, b[n].z, b[n].w);
-        if ((w + 1) % p.gw == 0) {
-          float s0, s1;
-          if (p.s_f32) {
-            const float* s = reinterpret_cast<const float*>(r + soff) + gr * 16;
-            s0 = s[g4]; s1 = s[g4 + 8];
-          } else {
-            const __nv_bfloat16* s = reinterpret_cast<const __nv_bfloat16*>(r + soff) + gr * 16;
-            s0 = __bfloat162float(s[g4]); s1 = __bfloat162float(s[g4 + 8]);
+          for (int n = 0; n < NT; ++n) xk[n] = x0[n] + (uint32_t)kb * 4 * xstep[n];
+          uint32_t z0 = 0xc1c0c1c0u, z1 = z0;  // -24, -24
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int i0 = w / GW, i1 = NG + w / GW;  // the group's place among the lane's scales: rows g, g + 8
+            if (w % GW == 0 && p.has_z) {
+              z0 = __byte_perm(r.z[i0 >> 1], 0, i0 & 1 ? 0x3232 : 0x1010);
+              z1 = __byte_perm(r.z[i1 >> 1], 0, i1 & 1 ? 0x3232 : 0x1010);
+            }
+            uint4 b[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              b[n] = *reinterpret_cast<const uint4*>(smem + xk[n]);
+              xk[n] += xstep[n];
+            }
+            const uint32_t zz[4] = {z0, z1, z0, z1};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t a[4] = {pair(w0[w], 2 * h, magic), pair(w1[w], 2 * h, magic), pair(w0[w], 2 * h + 1, magic), pair(w1[w], 2 * h + 1, magic)};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) a[i] = add2(a[i], zz[i]);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const uint32_t b0 = h ? b[n].z : b[n].x, b1 = h ? b[n].w : b[n].y;
+                // independent chains of sums, joined at the group's end: one chain would wait for itself
+                float* c = acc[n][kChains > 1 ? h : 0];
+                if (w % GW == 0 && (kChains > 1 || h == 0)) mma16816_first(c, a, b0, b1);
+                else mma16816(c, a, b0, b1);
+              }
+            }
+            if (w % GW == GW - 1) {
+              float s0, s1;
+              if (p.s_f32) {
+                s0 = __uint_as_float(r.s[i0]);
+                s1 = __uint_as_float(r.s[i1]);
+              } else {
+                s0 = i0 & 1 ? bf16_hi(r.s[i0 >> 1]) : bf16_lo(r.s[i0 >> 1]);
+                s1 = i1 & 1 ? bf16_hi(r.s[i1 >> 1]) : bf16_lo(r.s[i1 >> 1]);
+              }
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  float v = acc[n][0][i];
+#pragma unroll
+                  for (int k = 1; k < kChains; ++k) v += acc[n][k][i];
+                  tot[n][i] += (i < 2 ? s0 : s1) * v;
+                }
+            }
           }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            tot[n][0] += s0 * acc[n][0]; tot[n][1] += s0 * acc[n][1];
-            tot[n][2] += s1 * acc[n][2]; tot[n][3] += s1 * acc[n][3];
-            acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+          if (at + j + kAhead < r1) {
+            load(rec[j], src);
+            advance();
+          }
+          if (++kb == nk || at + j + 1 == r1) {
+            flush();
+            kb = 0;
+            ++u;
           }
         }
       }
-    }
-    float* mine = part + (size_t)(parity * kWarps + warp) * 16 * PC;
+      if (r0 == r1) flush();  // an empty run between two others of a tile
+      __syncthreads();
+      // A thread finishes an output: row r of the batch, which is row r % 16 of tile r / 16, for vector m.  Its parts are
+      // those of the warps whose runs touch the tile; the small terms are added first.
+      const bool done = kb_lo + nk == p.nkb;
+      for (int o = tid; o < nrow * mb; o += kThreads) {
+        const int m = o / nrow, r = o - m * nrow, row = (t0 - G.tile0) * 16 + r, tl = r >> 4;
+        if (row >= G.rows) continue;
+        const int wa = ((tl * nk + 1) * kWarps - 1) / nrec, np = ((tl + 1) * nk * kWarps - 1) / nrec - wa + 1;
+        const float* q = part + ((wa + tl) * 16 + (r & 15)) * PC + m * p.terms;
+        float y = kb_lo ? sums[o] : 0.f;
+        for (int w = 0; w < np; w += 4) {
+          float v[4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      mine[g4 * PC + n * 8 + 2 * t4] = tot[n][0];
-      mine[g4 * PC + n * 8 + 2 * t4 + 1] = tot[n][1];
-      mine[(g4 + 8) * PC + n * 8 + 2 * t4] = tot[n][2];
-      mine[(g4 + 8) * PC + n * 8 + 2 * t4 + 1] = tot[n][3];
-    }
-    __syncthreads();
-    for (int o = tid; o < 16 * mb; o += kThreads) {
-      const int row = o & 15, m = o >> 4, r = (tile - G.tile0) * 16 + row;
-      if (r >= G.rows) continue;
-      float y = 0.f;
-      for (int w = 0; w < kWarps; ++w)
-        for (int e = p.terms - 1; e >= 0; --e) y += part[((size_t)(parity * kWarps + w) * 16 + row) * PC + m * p.terms + e];
-      if (p.nw) y *= s_ss[m];
-      const long long at = (long long)(m0 + m) * G.ys + r;
-      if (p.x_f32) static_cast<float*>(G.y)[at] = y;
-      else static_cast<__nv_bfloat16*>(G.y)[at] = __float2bfloat16_rn(y);
+          for (int k = 0; k < 4; ++k) {
+            v[k] = 0.f;
+            if (w + k < np)
+              for (int e = p.terms - 1; e >= 0; --e) v[k] += q[(w + k) * 16 * PC + e];
+          }
+          y += v[0];
+          y += v[1];
+          y += v[2];
+          y += v[3];
+        }
+        if (!done) {
+          sums[o] = y;
+          continue;
+        }
+        if (p.nw) y *= rsqrtf(s_sum[m] / p.cols + p.eps);
+        const long long at = (long long)(m0 + m) * G.ys + row;
+        if (p.x_f32) static_cast<float*>(G.y)[at] = y;
+        else static_cast<__nv_bfloat16*>(G.y)[at] = __float2bfloat16_rn(y);
+      }
+      if (!done || t1 < last) __syncthreads();  // the parts and the vectors are read
     }
   }
 }
 
-size_t gemv_smem(int nkb, int mb, int terms, int nt) {
-  return (size_t)nkb * 4 * mb * terms * 64 + (size_t)2 * kWarps * 16 * (nt * 8 + 1) * 4;
-}
-
-template <int NT>
+template <int NT, int GW>
 cudaError_t launch(const Params& p, dim3 grid, size_t smem, cudaStream_t s) {
   static std::mutex mu;
   static size_t have[64] = {};
@@ -293,13 +528,44 @@ cudaError_t launch(const Params& p, dim3 grid, size_t smem, cudaStream_t s) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 64 || have[dev] < smem) {
-      e = cudaFuncSetAttribute(gemv_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      e = cudaFuncSetAttribute(gemv_kernel<NT, GW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (e != cudaSuccess) return e;
       if (dev < 64) have[dev] = smem;
     }
   }
-  gemv_kernel<NT><<<grid, kThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemv_kernel<NT, GW>, p);
+}
+template <int NT>
+cudaError_t launch_gw(const Params& p, int group, dim3 grid, size_t smem, cudaStream_t s) {
+  return group == 128 ? launch<NT, 4>(p, grid, smem, s) : group == 64 ? launch<NT, 2>(p, grid, smem, s) : launch<NT, 1>(p, grid, smem, s);
+}
+
+// How the work is cut, for one block an SM: sets mb, chunk and batch; returns the operand tiles of a warp.
+//   mb: at most 48 operand columns (6 tiles of accumulators), in even shares.
+//   batch: the tiles of a block, as far as 96 KB of parts hold.
+//   chunk: all columns if they fit the rest of 224 KB, else even shares of them.
+int plan(Params* p, int sms) {
+  const int parts = (p->M * p->terms + 47) / 48;
+  p->mb = (p->M + parts - 1) / parts;
+  int nt = (p->mb * p->terms + 7) / 8;
+  if (nt > 4) nt = 6;
+  const int own = (p->tiles + sms - 1) / sms, most = 96 * 1024 / (16 * (nt * 8 + 1) * 4) - kWarps + 1;
+  p->batch = own < most ? own : most;
+  for (int n = 1;; ++n) {
+    p->chunk = (p->nkb + n - 1) / n;
+    if (smem_of(p->chunk, p->nkb, p->mb * p->terms, nt, p->batch, p->mb).total <= 224 * 1024) return nt;
+  }
 }
 
 bool sizes_ok(int rows, int cols, int group, int scale_dtype) {
@@ -381,31 +647,30 @@ extern "C" int spd_q4_gemv(const spd_q4_group* groups, int32_t G, int32_t M, int
     }
     q4::Group& d = p.g[g];
     d.w = static_cast<const unsigned char*>(s.w); d.x = s.x; d.y = s.y; d.xs = s.x_stride; d.ys = s.y_stride;
-    d.rows = s.rows; d.tile0 = (int)tiles;
+    d.rows = s.rows;
+    d.vec = q4::aligned(s.x, 16) && (M == 1 || s.x_stride % (16 / (int)esz) == 0);
+    d.tile0 = (int)tiles;
     tiles += (s.rows + 15LL) / 16;
   }
-  if (tiles > 0x7fffffffLL) return spd_internal_fail(SPD_EINVAL, "spd_q4_gemv: too many rows");
-  p.G = G; p.M = M; p.cols = cols; p.nkb = (cols + 127) / 128; p.tiles = (int)tiles; p.gw = group / 32;
+  if (tiles > 0x3fffffffLL) return spd_internal_fail(SPD_EINVAL, "spd_q4_gemv: too many rows");
+  p.tiles = (int)tiles;
+  p.G = G; p.M = M; p.cols = cols; p.nkb = (cols + 127) / 128;
   p.rec = (int)q4::record_bytes(group, scale_dtype, has_zeros);
   p.s_f32 = scale_dtype == SPD_DTYPE_F32; p.has_z = has_zeros != 0; p.x_f32 = x_dtype == SPD_DTYPE_F32;
-  p.nw = nw; p.eps = eps;
+  p.nw = nw; p.eps = eps; p.nvec = q4::aligned(nw, 16);
   p.terms = p.x_f32 ? 3 : nw ? 2 : 1;
-  // vectors of a block: as many as shared memory and six operand tiles hold, in even shares
-  int mb = M;
-  while ((mb * p.terms > 48 || q4::gemv_smem(p.nkb, mb, p.terms, (mb * p.terms + 7) / 8) > 220 * 1024) && mb > 1) mb = (mb + 1) / 2;
-  p.mb = mb;
-  const int nt = (mb * p.terms + 7) / 8;
-  const size_t smem = q4::gemv_smem(p.nkb, mb, p.terms, nt <= 4 ? nt : 6);
-  const dim3 grid((unsigned)(tiles < 2 * num_sms() ? tiles : 2 * num_sms()), (unsigned)((M + mb - 1) / mb));
+  const int sms = num_sms(), nt = q4::plan(&p, sms);
+  const size_t smem = q4::smem_of(p.chunk, p.nkb, p.mb * p.terms, nt, p.batch, p.mb).total;
+  const dim3 grid((unsigned)(p.tiles < sms ? p.tiles : sms), (unsigned)((M + p.mb - 1) / p.mb));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(cuda_stream);
   cudaGetLastError();
   cudaError_t e;
   switch (nt) {
-    case 1: e = q4::launch<1>(p, grid, smem, s); break;
-    case 2: e = q4::launch<2>(p, grid, smem, s); break;
-    case 3: e = q4::launch<3>(p, grid, smem, s); break;
-    case 4: e = q4::launch<4>(p, grid, smem, s); break;
-    default: e = q4::launch<6>(p, grid, smem, s); break;
+    case 1: e = q4::launch_gw<1>(p, group, grid, smem, s); break;
+    case 2: e = q4::launch_gw<2>(p, group, grid, smem, s); break;
+    case 3: e = q4::launch_gw<3>(p, group, grid, smem, s); break;
+    case 4: e = q4::launch_gw<4>(p, group, grid, smem, s); break;
+    default: e = q4::launch_gw<6>(p, group, grid, smem, s); break;
   }
   if (e != cudaSuccess) {
     char msg[160];
