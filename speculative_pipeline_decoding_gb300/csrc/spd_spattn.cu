@@ -35,7 +35,7 @@
 namespace spd {
 namespace spa {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;   // most warps of a block of the rows kernel
 constexpr int kThreads = 32 * kWarps;
 constexpr int kHeads = 8;  // query heads of a block (the mma's 8 columns)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -46,7 +46,7 @@ struct Params {
   const int* lens;
   void* out;
   float* lse;
-  float* part;      // prefix parts: unnormalised O [slot][row of the unit][hd]
+  float* part;      // prefix parts: unnormalised O [slot][tile of the unit][hd / 4][row][4]
   float2* part_ml;  // their maximum and sum [slot][row of the unit]
   long long prefix_cap, max_seq;
   int P, B, hq, hkv, gq, hblocks;
@@ -54,6 +54,7 @@ struct Params {
   // prefix kernel: `units` row tiles (pairs) x nch chunks, cut into n_cta runs; the part of run i for unit u is slot i + u
   int units_per_kv, units, nch, n_cta;
   int use_prefix;
+  int row_cluster, parts;  // rows kernel: blocks of a sequence and kv head; most parts of a row
 };
 
 // first chunk of run i
@@ -112,10 +113,27 @@ __device__ __forceinline__ void tma3(void* dst, const CUtensorMap* map, int x, i
       ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t db, uint32_t id, bool accumulate) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-               " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(db), "r"(id),
-               "r"((uint32_t)accumulate)
+// The multiplying warp runs as a whole, so that descriptors stay in uniform registers; one elected lane issues.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t y;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(y));
+  return y;
+}
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t da, uint64_t db, uint32_t id, uint32_t accumulate) {
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+               " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(da), "l"(db), "r"(id),
+               "r"(accumulate), "r"(lead)
+               : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t db, uint32_t id, uint32_t accumulate) {
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+               " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(db), "r"(id),
+               "r"(accumulate), "r"(lead)
+               : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t lead, uint64_t* bar) {
+  asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+               " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)), "r"(lead)
                : "memory");
 }
 // V as the second operand, keys along K: rows of 128 bytes, 8-key groups 1024 B apart, the halves of hd one tile apart
@@ -197,9 +215,12 @@ prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMa
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tc::alloc_cols(&s_tmem, 512);
+  if (warp == kCopyWarp && (tid & 31) < 2)
+    asm volatile("prefetch.tensormap [%0];" ::"l"((tid & 31) ? &maps.v : &maps.k));
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
+  pdl_wait();
   pdl_trigger();  // the rows kernel may start its own keys beside this one
   const uint32_t tm = s_tmem;
   const long long total = (long long)p.units * p.nch;
@@ -251,83 +272,90 @@ prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMa
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
-    if ((tid & 31) == 0) {
-      uint32_t n_stage = 0;            // stages taken so far, K and V in turn
-      uint32_t ph_q[NS] = {}, ph_p[NS] = {}, ph_f[NS] = {};
-      bool ok = true;
-      constexpr uint32_t id_s = idesc(kTile, 0), id_o = idesc(HD, 1);
-      auto scores = [&](int i, uint32_t stage) {
-        uint64_t dk = tc::sdesc(tc::su32(ring + stage * C::kTB)), dq = tc::sdesc(tc::su32(sq + i * TERMS * C::kTB));
-        opaque(dk);  // descriptors are added up in place: hoisted out of the loop they would spill
-        opaque(dq);
+    const uint32_t lead = elect_one();
+    uint32_t st = 0, ph = 0;         // the next stage to take, K and V in turn
+    uint32_t ph_q = 0, ph_p = 0, ph_f = 0;  // one bit a tile
+    bool ok = true;
+    constexpr uint32_t id_s = idesc(kTile, 0), id_o = idesc(HD, 1);
+    const uint64_t dq0 = tc::sdesc(tc::su32(sq)), dk0 = tc::sdesc(tc::su32(ring)), dv0 = desc_v(tc::su32(ring));
+    auto take = [&](uint32_t& at, uint32_t& parity) {
+      at = st;
+      parity = ph;
+      if (++st == ST) { st = 0; ph ^= 1; }
+    };
+    auto await = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity, &s_fail)) != 0; };
+    auto scores = [&](int i, uint32_t stage) {
+      uint64_t dk = dk0 + (uint64_t)(stage * (C::kTB >> 4)), dq = dq0 + (uint64_t)(i * (TERMS * C::kTB >> 4));
+      opaque(dk);  // descriptors are added up in place: hoisted out of the loop they would spill
+      opaque(dq);
 #pragma unroll
-        for (int e = TERMS - 1; e >= 0; --e)  // the small terms first
+      for (int e = TERMS - 1; e >= 0; --e)  // the small terms first
 #pragma unroll
-          for (int ks = 0; ks < HD / 16; ++ks) {
-            const int off = (ks >> 2) * kTile * 128 + (ks & 3) * 32;
-            tc::mma(tm + C::s_col(i), dq + ((e * C::kTB + off) >> 4), dk + (off >> 4), id_s, e < TERMS - 1 || ks > 0);
-          }
-        tc::commit(&s_full[i]);
-      };
-      for (long long w = w0; w < w1 && ok;) {
-        const Piece x = piece_at(w);
-        for (int i = 0; i < x.nt && ok; ++i) {
-          ok = wait(&q_ready[i], ph_q[i], &s_fail);
-          ph_q[i] ^= 1;
+        for (int ks = 0; ks < HD / 16; ++ks) {
+          const int off = (ks >> 2) * kTile * 128 + (ks & 3) * 32;
+          mma_ss(lead, tm + C::s_col(i), dq + ((e * C::kTB + off) >> 4), dk + (off >> 4), id_s, e < TERMS - 1 || ks > 0);
         }
-        if (!ok) break;
-        tc::fence_after();
-        uint32_t kst = n_stage % ST;
-        ok = wait(&full[kst], (n_stage / ST) & 1, &s_fail);
-        if (!ok) break;
-        ++n_stage;
-        for (int i = 0; i < x.nt; ++i) scores(i, kst);
-        tc::commit(&empty[kst]);
-        for (int c = x.c0; c < x.c1 && ok; ++c) {
-          const uint32_t vst = n_stage % ST, vph = (n_stage / ST) & 1;
-          ++n_stage;
-          const bool more = c + 1 < x.c1;
-          const uint32_t k2 = n_stage % ST, kph = (n_stage / ST) & 1;
-          if (more) ++n_stage;
-          for (int i = 0; i < x.nt && ok; ++i) {
-            if (NS == 1 && more) {  // P does not lie over S: the next scores run during this chunk's softmax
-              ok = wait(&s_free[i], ph_f[i], &s_fail) && wait(&full[k2], kph, &s_fail);
-              ph_f[i] ^= 1;
-              if (!ok) break;
-              tc::fence_after();
-              scores(i, k2);
-              tc::commit(&empty[k2]);
-            }
-            ok = wait(&p_ready[i], ph_p[i], &s_fail);
-            ph_p[i] ^= 1;
-            if (ok && i == 0) ok = wait(&full[vst], vph, &s_fail);
+      commit_if(lead, &s_full[i]);
+    };
+    for (long long w = w0; w < w1 && ok;) {
+      const Piece x = piece_at(w);
+      for (int i = 0; i < x.nt && ok; ++i) {
+        ok = await(&q_ready[i], ph_q >> i & 1);
+        ph_q ^= 1u << i;
+      }
+      if (!ok) break;
+      tc::fence_after();
+      uint32_t kst, kph;
+      take(kst, kph);
+      ok = await(&full[kst], kph);
+      if (!ok) break;
+      for (int i = 0; i < x.nt; ++i) scores(i, kst);
+      commit_if(lead, &empty[kst]);
+      for (int c = x.c0; c < x.c1 && ok; ++c) {
+        const bool more = c + 1 < x.c1;
+        uint32_t vst, vph, k2 = 0, k2ph = 0;
+        take(vst, vph);
+        if (more) take(k2, k2ph);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          if (i >= x.nt || !ok) break;
+          if (NS == 1 && more) {  // P does not lie over S: the next scores run during this chunk's softmax
+            ok = await(&s_free[i], ph_f & 1) && await(&full[k2], k2ph);
+            ph_f ^= 1;
             if (!ok) break;
             tc::fence_after();
-            uint64_t dv = desc_v(tc::su32(ring + vst * C::kTB));
-            opaque(dv);
-#pragma unroll
-            for (int e = TERMS - 1; e >= 0; --e)
-#pragma unroll
-              for (int ks = 0; ks < kTile / 16; ++ks)
-                mma_ts(tm + C::o_col(i), tm + C::p_col(i) + e * 64 + ks * 8, dv + ((ks * 2048) >> 4), id_o,
-                       c > x.c0 || e < TERMS - 1 || ks > 0);
-            if (i == x.nt - 1) tc::commit(&empty[vst]);
-            if (!more) tc::commit(&o_full[i]);
-            if (NS == 2 && more) {
-              if (i == 0) ok = wait(&full[k2], kph, &s_fail);
-              if (!ok) break;
-              scores(i, k2);  // after this tile's P V, which reads what it overwrites
-              if (i == x.nt - 1) tc::commit(&empty[k2]);
-            }
-            if (NS == 1 && more) tc::commit(&pv_done);
+            scores(i, k2);
+            commit_if(lead, &empty[k2]);
           }
+          ok = await(&p_ready[i], ph_p >> i & 1);
+          ph_p ^= 1u << i;
+          if (ok && i == 0) ok = await(&full[vst], vph);
+          if (!ok) break;
+          tc::fence_after();
+          uint64_t dv = dv0 + (uint64_t)(vst * (C::kTB >> 4));
+          opaque(dv);
+#pragma unroll
+          for (int e = TERMS - 1; e >= 0; --e)
+#pragma unroll
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              mma_ts(lead, tm + C::o_col(i), tm + C::p_col(i) + e * 64 + ks * 8, dv + ((ks * 2048) >> 4), id_o,
+                     c > x.c0 || e < TERMS - 1 || ks > 0);
+          if (i == x.nt - 1) commit_if(lead, &empty[vst]);
+          if (!more) commit_if(lead, &o_full[i]);
+          if (NS == 2 && more) {
+            if (i == 0) ok = await(&full[k2], k2ph);
+            if (!ok) break;
+            scores(i, k2);  // after this tile's P V, which reads what it overwrites
+            if (i == x.nt - 1) commit_if(lead, &empty[k2]);
+          }
+          if (NS == 1 && more) commit_if(lead, &pv_done);
         }
-        w += x.c1 - x.c0;
       }
-      if (!ok) {  // the products in flight end before the block leaves
-        tc::commit(&drain);
-        mbar_wait_bounded(&drain, 0);
-      }
+      w += x.c1 - x.c0;
+    }
+    if (!ok) {  // the products in flight end before the block leaves
+      commit_if(lead, &drain);
+      mbar_wait_bounded(&drain, 0);
     }
     __syncwarp();
   }
@@ -348,7 +376,7 @@ prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMa
         const int b = row / p.gq, h = x.kh * p.gq + row % p.gq;
         const long long at = ((long long)b * p.hq + h) * HD;
         unsigned char* dst = sq + slot * TERMS * C::kTB;
-#pragma unroll 4
+#pragma unroll (TERMS == 1 ? HD / 8 : 4)
         for (int e = 0; e < HD; e += 8) {
           if (TERMS == 1) {
             const uint4 v = valid ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at + e) : make_uint4(0, 0, 0, 0);
@@ -448,17 +476,18 @@ prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMa
       if (!ok) break;
       tc::fence_after();
       // unnormalised O and (m, l) of the row
-      const long long part_row = (long long)(blockIdx.x + x.u) * (NS * kTile) + slot * kTile + r;
-      float* po = p.part + part_row * HD;
+      const long long part_tile = (long long)(blockIdx.x + x.u) * NS + slot;
+      float* po = p.part + part_tile * (kTile * HD) + r * 4;  // [element / 4][row][4]: neighbours write neighbours
 #pragma unroll
       for (int j = 0; j < HD; j += 32) {
         uint32_t ov[32];
         tc::load_rows(tm + C::o_col(slot) + j, warp, ov);
         if (valid)
 #pragma unroll
-          for (int t = 0; t < 32; t += 4) *reinterpret_cast<uint4*>(po + j + t) = make_uint4(ov[t], ov[t + 1], ov[t + 2], ov[t + 3]);
+          for (int t = 0; t < 32; t += 4)
+            *reinterpret_cast<uint4*>(po + (j + t) * kTile) = make_uint4(ov[t], ov[t + 1], ov[t + 2], ov[t + 3]);
       }
-      p.part_ml[part_row] = make_float2(m, l);
+      p.part_ml[part_tile * kTile + r] = make_float2(m, l);
     }
     if (!ok)  // a wait gave up: the rows of this block's pieces come out NaN
       for (long long w = w0; w < w1;) {
@@ -473,66 +502,152 @@ prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMa
 }
 
 
+// The sum over the cluster's blocks goes through their shared memory.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t remote_addr(const void* p, int rank) {  // the same place in another block of the cluster
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float remote(const float* p, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 remote4(const float* p, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(remote_addr(p, rank)) : "memory");
+  return v;
+}
+
+// Shared memory of the rows kernel: the warps' rings (afterwards O, maxima and sums of the warps), the weights of the parts,
+// the barriers.
+constexpr int kRing = 3;                                       // steps of 16 keys that a warp has under way
+constexpr int stage_bytes(int hd) { return 2 * 16 * hd * 2; }  // K and V
+__host__ __device__ constexpr int rows_smem(int warps, int hd, int parts) {
+  return warps * kRing * stage_bytes(hd) + (kHeads * parts * 4 + 7) / 8 * 8 + warps * kRing * 8;
+}
+
 template <int HD, int TERMS>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, TERMS == 1 ? 3 : 2) rows_kernel(const __grid_constant__ Params p) {
   constexpr int KI = HD / 32;  // 16-byte pieces of a key a lane reads
-  extern __shared__ __align__(16) unsigned char smem[];
-  float* s_o = reinterpret_cast<float*>(smem);  // [warp][head][HD]
-  __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
+  constexpr int NS = Cfg<HD, TERMS>::kSlots;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int W = blockDim.x >> 5;
+  float* s_o = reinterpret_cast<float*>(smem);  // [warp][head][HD], over the rings
+  float* s_m = s_o + W * kHeads * HD;           // [warp][head]
+  float* s_l = s_m + W * kHeads;                // [warp][head]
+  float* s_w = reinterpret_cast<float*>(smem + W * kRing * stage_bytes(HD));  // [head][part]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + rows_smem(W, HD, p.parts) - W * kRing * 8);
+  static_assert(kRing * stage_bytes(HD) >= kHeads * (HD + 2) * 4, "a warp's sums fit over its ring");
+  __shared__ float s_sum[kHeads];
+  __shared__ int s_fail;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int hb = blockIdx.x % p.hblocks, kh = blockIdx.x / p.hblocks % p.hkv, b = blockIdx.x / p.hblocks / p.hkv;
+  const int CS = p.row_cluster, rank = blockIdx.x % CS, pair = blockIdx.x / CS;
+  const int hb = pair % p.hblocks, kh = pair / p.hblocks % p.hkv, b = pair / p.hblocks / p.hkv;
   const int h0 = kh * p.gq + hb * kHeads, nh = min(kHeads, p.gq - hb * kHeads);
+  unsigned char* ring = smem + warp * kRing * stage_bytes(HD);
+  uint64_t* bar = bars + warp * kRing;
+  if (lane == 0) {
+    for (int i = 0; i < kRing; ++i) mbar_init(&bar[i], 1);
+    fence_mbar_init();
+  }
+  if (tid == 0) s_fail = 0;
   const int len = p.max_seq > 0 ? p.lens[b] : 0;
   const bool bad = len < 0 || len > p.max_seq;
-
+  const int P = p.use_prefix ? 0 : p.P;  // prefix keys that this kernel reads itself
+  const int nkeys = bad ? 0 : P + len;
+  const int key_step = CS * W * 16;
+  int key0 = (rank * W + warp) * 16;
+  const __nv_bfloat16* own_k = p.kc + ((long long)b * p.hkv + kh) * p.max_seq * HD;
+  const __nv_bfloat16* own_v = p.vc + ((long long)b * p.hkv + kh) * p.max_seq * HD;
+  const __nv_bfloat16* pre_k = p.pk + (long long)kh * p.prefix_cap * HD;
+  const __nv_bfloat16* pre_v = p.pv + (long long)kh * p.prefix_cap * HD;
+  // the rows of 16 keys from k0, those that exist, into a stage: K [16][HD], V [16][HD]
+  const uint64_t pol = l2_evict_first_policy();
+  auto fetch = [&](int st, int k0) {  // lane 0
+    unsigned char* dst = ring + st * stage_bytes(HD);
+    const int n = min(16, nkeys - k0), a = max(0, min(n, P - k0));  // a of them in the prefix
+    mbar_arrive_expect_tx(&bar[st], (uint32_t)n * HD * 4);
+    if (a > 0) {
+      bulk_g2s(dst, pre_k + (long long)k0 * HD, a * HD * 2, &bar[st], pol);
+      bulk_g2s(dst + 16 * HD * 2, pre_v + (long long)k0 * HD, a * HD * 2, &bar[st], pol);
+    }
+    if (a < n) {
+      const long long at = (long long)(k0 + a - P) * HD;
+      bulk_g2s(dst + a * HD * 2, own_k + at, (n - a) * HD * 2, &bar[st], pol);
+      bulk_g2s(dst + (16 + a) * HD * 2, own_v + at, (n - a) * HD * 2, &bar[st], pol);
+    }
+  };
+  if (lane == 0)
+    for (int i = 0; i < kRing; ++i)
+      if (key0 + i * key_step < nkeys) fetch(i, key0 + i * key_step);
   // Q^T as the second operand: head g, elements 32 i + 8 t + 4 s + {0, 1}, {2, 3}
   uint32_t qb[TERMS][KI][2][2];
 #pragma unroll
   for (int i = 0; i < KI; ++i) {
+    const long long at = ((long long)b * p.hq + h0 + min(g, nh - 1)) * HD + 32 * i + 8 * t;
     float x[8];
-    const long long at = ((long long)b * p.hq + h0 + g) * HD + 32 * i + 8 * t;
+    if (TERMS > 1) {
+      const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at);
+      const float4 c = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at + 4);
+      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = c.x; x[5] = c.y; x[6] = c.z; x[7] = c.w;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      x[j] = g >= nh ? 0.f
-                     : TERMS > 1 ? static_cast<const float*>(p.q)[at + j] : __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[at + j]);
+      for (int e = 0; e < TERMS; ++e)
 #pragma unroll
-    for (int e = 0; e < TERMS; ++e)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        qb[e][i][s][0] = take_pair(x[4 * s], x[4 * s + 1]);
-        qb[e][i][s][1] = take_pair(x[4 * s + 2], x[4 * s + 3]);
-      }
+        for (int s = 0; s < 2; ++s) {
+          qb[e][i][s][0] = take_pair(x[4 * s], x[4 * s + 1]);
+          qb[e][i][s][1] = take_pair(x[4 * s + 2], x[4 * s + 3]);
+        }
+    } else {
+      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at);
+      qb[0][i][0][0] = a.x; qb[0][i][0][1] = a.y; qb[0][i][1][0] = a.z; qb[0][i][1][1] = a.w;
+    }
   }
   float o[HD / 16][4];
 #pragma unroll
   for (int e = 0; e < HD / 16; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // heads 2 t, 2 t + 1
 
-  const int P = p.use_prefix ? 0 : p.P;  // prefix keys that this kernel reads itself
-  const int nkeys = bad ? 0 : P + len;
-  for (int key0 = warp * 16; key0 < nkeys; key0 += kWarps * 16) {
-    // keys of this lane: as rows g, g + 8 of K and as 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of V
-    auto row = [&](const __nv_bfloat16* pre, const __nv_bfloat16* own, int key) {
-      key = min(key, nkeys - 1);
-      return key < P ? pre + ((long long)kh * p.prefix_cap + key) * HD
-                     : own + (((long long)b * p.hkv + kh) * p.max_seq + (key - P)) * HD;
-    };
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    const __nv_bfloat16 *ka = row(p.pk, p.kc, key0 + g) + 8 * t, *kb = row(p.pk, p.kc, key0 + g + 8) + 8 * t;
-#pragma unroll
-    for (int i = 0; i < KI; ++i) {
-      const uint4 a = *reinterpret_cast<const uint4*>(ka + 32 * i), c = *reinterpret_cast<const uint4*>(kb + 32 * i);
-#pragma unroll
-      for (int e = TERMS - 1; e >= 0; --e) {
-        mma16816(s, a.x, c.x, a.y, c.y, qb[e][i][0][0], qb[e][i][0][1]);
-        mma16816(s, a.z, c.z, a.w, c.w, qb[e][i][1][0], qb[e][i][1][1]);
-      }
+  __syncwarp();  // the barriers are set up
+  bool ok = true;
+  int st = 0;
+  uint32_t ph = 0;
+  for (; key0 < nkeys; key0 += key_step) {
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[st], ph)) != 0;
+    unsigned char* stage = ring + st * stage_bytes(HD);
+    if (nkeys - key0 < 16) {  // rows that no key fills weigh nothing, but must not hold NaN
+      for (int i = (nkeys - key0) * (HD / 8) + lane; i < 16 * (HD / 8); i += 32)
+        reinterpret_cast<uint4*>(stage + 16 * HD * 2)[i] = make_uint4(0, 0, 0, 0);
+      __syncwarp();
     }
-    // s: (key g, heads 2t, 2t+1), (key g + 8, heads 2t, 2t+1)
-    float al[2];
-    float pr[4];
+    uint4 kr[2][KI], vr[4][HD / 64];  // keys g, g + 8; keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] = key0 + g + 8 * (j >> 1) < nkeys ? s[j] * p.scale_log2 : -INFINITY;
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < KI; ++i) kr[j][i] = *reinterpret_cast<const uint4*>(stage + (g + 8 * j) * HD * 2 + 16 * t + 64 * i);
+    // the hardware's sums drop bits: the small terms first, in chains of their own
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = TERMS - 1; e >= 0; --e)
+#pragma unroll
+      for (int i = 0; i < KI; ++i) {
+        float* c = e > 0 ? s2 : s;
+        mma16816(c, kr[0][i].x, kr[1][i].x, kr[0][i].y, kr[1][i].y, qb[e][i][0][0], qb[e][i][0][1]);
+        mma16816(c, kr[0][i].z, kr[1][i].z, kr[0][i].w, kr[1][i].w, qb[e][i][1][0], qb[e][i][1][1]);
+      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int c = 0; c < HD / 64; ++c)
+        vr[j][c] = *reinterpret_cast<const uint4*>(stage + (16 + 2 * t + (j & 1) + 8 * (j >> 1)) * HD * 2 + 16 * g + 128 * c);
+    // s: (key g, heads 2t, 2t+1), (key g + 8, heads 2t, 2t+1)
+    float al[2], pr[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = key0 + g + 8 * (j >> 1) < nkeys ? (s[j] + s2[j]) * p.scale_log2 : -INFINITY;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       float mx = fmaxf(s[j], s[j + 2]);
@@ -546,9 +661,11 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
       pr[j + 2] = ex2(s[j + 2] - mu);
       l[j] = l[j] * al[j] + pr[j] + pr[j + 2];
     }
+    if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
 #pragma unroll
-    for (int e = 0; e < HD / 16; ++e) {
-      o[e][0] *= al[0]; o[e][1] *= al[1]; o[e][2] *= al[0]; o[e][3] *= al[1];
+      for (int e = 0; e < HD / 16; ++e) {
+        o[e][0] *= al[0]; o[e][1] *= al[1]; o[e][2] *= al[0]; o[e][3] *= al[1];
+      }
     }
     uint32_t pb[TERMS][2];
 #pragma unroll
@@ -556,29 +673,38 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
       pb[e][0] = movm(take_pair(pr[0], pr[1]));
       pb[e][1] = movm(take_pair(pr[2], pr[3]));
     }
-    const __nv_bfloat16* vr[4] = {row(p.pv, p.vc, key0 + 2 * t), row(p.pv, p.vc, key0 + 2 * t + 1), row(p.pv, p.vc, key0 + 2 * t + 8),
-                                  row(p.pv, p.vc, key0 + 2 * t + 9)};
     // element e of this lane's two pieces of 8: rows g -> g * 8 + e and g + 8 -> 64 + g * 8 + e (hd 128), or
     // g * 8 + 2 e and g * 8 + 2 e + 1 (hd 64)
-    uint32_t w[4][HD / 16];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int c = 0; c < HD / 64; ++c) {
-        const uint4 x = *reinterpret_cast<const uint4*>(vr[k] + 64 * c + 8 * g);
-        w[k][4 * c] = x.x; w[k][4 * c + 1] = x.y; w[k][4 * c + 2] = x.z; w[k][4 * c + 3] = x.w;
-      }
+    auto word = [&](int k, int i) {
+      const uint4& x = vr[k][i >> 2];
+      return (i & 3) == 0 ? x.x : (i & 3) == 1 ? x.y : (i & 3) == 2 ? x.z : x.w;
+    };
     auto take = [&](int k, int el) {  // elements el of keys k and k + 1
-      return __byte_perm(w[k][el >> 1], w[k + 1][el >> 1], el & 1 ? 0x7632 : 0x5410);
+      return __byte_perm(word(k, el >> 1), word(k + 1, el >> 1), el & 1 ? 0x7632 : 0x5410);
     };
 #pragma unroll
     for (int e = 0; e < HD / 16; ++e) {
       const int lo = HD == 128 ? e : 2 * e, hi = HD == 128 ? e + 8 : 2 * e + 1;
       const uint32_t a0 = take(0, lo), a1 = take(0, hi), a2 = take(2, lo), a3 = take(2, hi);
+      if (TERMS == 1) {
+        mma16816(o[e], a0, a1, a2, a3, pb[0][0], pb[0][1]);
+      } else {  // this step's sum apart from the total, which is added to with rounding
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int x = TERMS - 1; x >= 0; --x) mma16816(o[e], a0, a1, a2, a3, pb[x][0], pb[x][1]);
+        for (int x = TERMS - 1; x >= 0; --x) mma16816(c, a0, a1, a2, a3, pb[x][0], pb[x][1]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[e][x] += c[x];
+      }
     }
+    __syncwarp();  // every lane has read the stage
+    if (lane == 0 && ok && key0 + kRing * key_step < nkeys) fetch(st, key0 + kRing * key_step);
+    if (++st == kRing) { st = 0; ph ^= 1; }
   }
+  if (!ok) {  // a wait gave up: the copies in flight land, the row comes out NaN
+    for (int i = 0; i < kRing; ++i) mbar_wait_bounded(&bar[(st + i) % kRing], ph ^ (st + i >= kRing), 10000000ull);
+    s_fail = 1;
+  }
+  __syncthreads();  // the rings are read, and the sums may lie over them
   // this warp's part
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -586,8 +712,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
     l[j] += __shfl_xor_sync(0xffffffffu, l[j], 8);
     l[j] += __shfl_xor_sync(0xffffffffu, l[j], 16);
     if (g == 0) {
-      s_m[warp][2 * t + j] = m[j];
-      s_l[warp][2 * t + j] = l[j];
+      s_m[warp * kHeads + 2 * t + j] = m[j];
+      s_l[warp * kHeads + 2 * t + j] = l[j];
     }
   }
 #pragma unroll
@@ -597,51 +723,157 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
     d0[lo] = o[e][0]; d0[HD + lo] = o[e][1]; d0[hi] = o[e][2]; d0[HD + hi] = o[e][3];
   }
   __syncthreads();
-  pdl_wait();  // the prefix kernel's parts are there (every block waits, so that this grid ends after that one)
-  constexpr int NS = Cfg<HD, TERMS>::kSlots;
-  const bool none = p.P == 0 && len == 0;
-  for (int i = tid; i < nh * HD; i += kThreads) {
-    const int h = i / HD, d = i % HD;
-    // the parts of this row: slots first + u .. last + u of its unit
-    const int row = b * p.gq + hb * kHeads + h, u = kh * p.units_per_kv + row / (NS * kTile);
-    int first = 0, last = -1;
-    if (p.use_prefix) {
-      const long long total = (long long)p.units * p.nch;
-      first = (int)((((long long)u * p.nch + 1) * p.n_cta - 1) / total);
-      last = (int)(((long long)(u + 1) * p.nch * p.n_cta - 1) / total);
+  // The parts of a row: W warps of this block, or the blocks of the cluster (each first adds up its own warps, in the place
+  // of its first), then the prefix kernel's.
+  auto combine = [&](float& y, float w, float v) { y = fmaf(w, v, y); };
+  if (CS > 1) {
+    for (int i = tid; i < nh * (HD / 4); i += blockDim.x) {
+      const int h = i / (HD / 4), d = i % (HD / 4) * 4;
+      float mx = -INFINITY;
+      for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[w * kHeads + h]);
+      const float mu = mx == -INFINITY ? 0.f : mx;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < W; ++w) {
+        const float a = ex2(s_m[w * kHeads + h] - mu);
+        const float4 v = *reinterpret_cast<const float4*>(s_o + (w * kHeads + h) * HD + d);
+        combine(y.x, a, v.x); combine(y.y, a, v.y); combine(y.z, a, v.z); combine(y.w, a, v.w);
+      }
+      *reinterpret_cast<float4*>(s_o + h * HD + d) = y;  // read by this thread only
     }
-    const long long at0 = (long long)(first + u) * (NS * kTile) + row % (NS * kTile);
-    float mx = -INFINITY;
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][h]);
-    for (int j = 0; j <= last - first; ++j) mx = fmaxf(mx, __ldcg(&p.part_ml[at0 + (long long)j * NS * kTile]).x);
-    const float mu = mx == -INFINITY ? 0.f : mx;
-    float lt = 0.f, ot = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      const float a = ex2(s_m[w][h] - mu);
-      lt += s_l[w][h] * a;
-      ot += s_o[(w * kHeads + h) * HD + d] * a;
+    __syncthreads();
+    if (tid < nh) {
+      float mx = -INFINITY, lt = 0.f;
+      for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[w * kHeads + tid]);
+      const float mu = mx == -INFINITY ? 0.f : mx;
+      for (int w = 0; w < W; ++w) lt += s_l[w * kHeads + tid] * ex2(s_m[w * kHeads + tid] - mu);
+      s_m[tid] = mx;
+      s_l[tid] = lt;
     }
-#pragma unroll 4
-    for (int j = 0; j <= last - first; ++j) {
-      const long long at = at0 + (long long)j * NS * kTile;
-      const float2 ml = __ldcg(&p.part_ml[at]);
-      const float a = ex2(ml.x - mu);
-      lt += ml.y * a;
-      ot += __ldcg(&p.part[at * HD + d]) * a;
-    }
-    const float y = bad ? NAN : none ? 0.f : ot / lt;
-    const long long at = ((long long)b * p.hq + h0 + h) * HD + d;
-    if (TERMS > 1) static_cast<float*>(p.out)[at] = y;
-    else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
-    if (d == 0 && p.lse) p.lse[(long long)b * p.hq + h0 + h] = bad ? NAN : none ? -INFINITY : mx * kLn2 + logf(lt);
+    cluster_sync();
   }
+  pdl_wait();  // the prefix kernel's parts are there (every block waits, so that this grid ends after that one)
+  const int nw = CS > 1 ? CS : W;
+  const bool none = p.P == 0 && len == 0;
+  if (rank == 0) {
+    // the row's parts of the prefix: slots first + u .. last + u of its unit
+    __shared__ long long s_at[kHeads];
+    __shared__ int s_np[kHeads];
+    auto prefix_parts = [&](int h, int* np) {
+      const int prow = b * p.gq + hb * kHeads + h, u = kh * p.units_per_kv + prow / (NS * kTile);
+      if (!p.use_prefix) {
+        *np = 0;
+        return 0LL;
+      }
+      const long long total = (long long)p.units * p.nch;
+      int first;
+      if (total * p.n_cta < 0x7fffffffLL) {  // 32-bit divisions where they do
+        first = ((u * p.nch + 1) * p.n_cta - 1) / (int)total;
+        *np = ((u + 1) * p.nch * p.n_cta - 1) / (int)total - first + 1;
+      } else {
+        first = (int)((((long long)u * p.nch + 1) * p.n_cta - 1) / total);
+        *np = (int)(((long long)(u + 1) * p.nch * p.n_cta - 1) / total) - first + 1;
+      }
+      return (long long)(first + u) * (NS * kTile) + prow % (NS * kTile);
+    };
+    // the first parts of this thread's first output on their way while the weights are formed
+    constexpr int kFirst = 12;
+    float4 early[kFirst];
+    {
+      int np;
+      const int h = tid % nh, d = tid / nh * 4;
+      const long long at = prefix_parts(h, &np);
+      const float* src = p.part + at / kTile * (kTile * HD) + d * kTile + at % kTile * 4;
+#pragma unroll
+      for (int x = 0; x < kFirst; ++x)
+        if (x < np && d < HD) early[x] = __ldcg(reinterpret_cast<const float4*>(src + (long long)x * NS * kTile * HD));
+    }
+    // weights of the parts, a warp a head
+    for (int h = warp; h < nh; h += W) {
+      int np;
+      const long long at = prefix_parts(h, &np);
+      const float2* ml = p.part_ml + at;
+      float* wt = s_w + h * p.parts;
+      float mx = -INFINITY, lt = 0.f;
+      for (int j0 = 0; j0 < nw + np; j0 += 32) {
+        const int j = j0 + lane;
+        float2 v = make_float2(-INFINITY, 0.f);
+        if (j < nw) v = CS > 1 ? make_float2(remote(&s_m[h], j), remote(&s_l[h], j)) : make_float2(s_m[j * kHeads + h], s_l[j * kHeads + h]);
+        else if (j < nw + np) v = __ldcg(ml + (long long)(j - nw) * NS * kTile);
+        float mn = v.x;
+#pragma unroll
+        for (int x = 16; x; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
+        mn = fmaxf(mn, mx);
+        const float mu = mn == -INFINITY ? 0.f : mn;
+        lt = lt * ex2(mx - mu) + v.y * ex2(v.x - mu);  // of this lane's parts
+        mx = mn;
+        if (j < nw + np) wt[j] = v.x;
+      }
+#pragma unroll
+      for (int x = 16; x; x >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, x);
+      const float mu = mx == -INFINITY ? 0.f : mx;
+      for (int j = lane; j < nw + np; j += 32) wt[j] = ex2(wt[j] - mu);
+      if (lane == 0) {
+        s_at[h] = at;
+        s_np[h] = np;
+        s_sum[h] = lt;
+        if (p.lse) p.lse[(long long)b * p.hq + h0 + h] = bad ? NAN : none ? -INFINITY : mx * kLn2 + logf(lt);
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < nh * (HD / 4); i += blockDim.x) {
+      const int h = i % nh, d = i / nh * 4;  // neighbours: the heads' rows lie side by side in a part
+      const float* wt = s_w + h * p.parts;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add = [&](float w, const float4& v) {
+        combine(y.x, w, v.x); combine(y.y, w, v.y); combine(y.z, w, v.z); combine(y.w, w, v.w);
+      };
+      const int np = s_np[h];
+      const float* src = p.part + s_at[h] / kTile * (kTile * HD) + d * kTile + s_at[h] % kTile * 4;
+      int done = 0;
+      if (i == tid) {
+#pragma unroll
+        for (int x = 0; x < kFirst; ++x)
+          if (x < np) add(wt[nw + x], early[x]);
+        done = kFirst;
+      }
+      for (int j = done; j < np; j += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (j + x < np) v[x] = __ldcg(reinterpret_cast<const float4*>(src + (long long)(j + x) * NS * kTile * HD));
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (j + x < np) add(wt[nw + j + x], v[x]);
+      }
+      float4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)  // nw is at most 8
+        if (j < nw) v[j] = CS > 1 ? remote4(s_o + h * HD + d, j) : *reinterpret_cast<const float4*>(s_o + (j * kHeads + h) * HD + d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < nw) add(wt[j], v[j]);
+      const float inv = 1.0f / s_sum[h];
+      y.x *= inv; y.y *= inv; y.z *= inv; y.w *= inv;
+      if (bad || s_fail) y = make_float4(NAN, NAN, NAN, NAN);
+      else if (none) y = make_float4(0.f, 0.f, 0.f, 0.f);
+      const long long at = ((long long)b * p.hq + h0 + h) * HD + d;
+      if (TERMS > 1) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = y;
+      } else {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      }
+    }
+  }
+  if (CS > 1) cluster_sync();  // nobody reads this block's shared memory any more
 }
 
-// Prefix keys through the tensor cores, or read by the rows kernel of every sequence.
-bool prefix_pays(int B, int hkv, int hd, int P) {
-  (void)B; (void)hkv; (void)hd;
-  return P > 0;
-}
+// Prefix keys through the tensor cores, or read by the rows kernel of every sequence: the tensor cores' part costs some 8 us
+// before it gains anything.  Bytes that all sequences together would read: at 17 MB (32 x 128 keys, 8 kv heads) 7.8 us
+// directly and 11.0 through the tensor cores, at 34 MB (4 x 2048) 11.5 and 12.3, at 67 MB (16 x 1024) 15.7 and 11.8, at 155 MB
+// (17 x 1111, 16 kv heads, fp32 queries) 32 and 25.
+bool prefix_pays(int B, int hkv, int hd, int P) { return (long long)B * hkv * P * hd * 4 > (48LL << 20); }
 
 // Units, runs and chunks of the prefix kernel; `ns` row tiles a unit.
 void prefix_geometry(int rows, int hkv, int P, int ns, int sms, Params* p) {
@@ -681,40 +913,71 @@ cudaError_t encode_map(CUtensorMap* out, const void* base, int hd, int P, int ca
 template <int HD, int TERMS>
 cudaError_t launch(Params& p, void* workspace, cudaStream_t s) {
   using C = Cfg<HD, TERMS>;
+  static std::mutex mu;
+  static bool set[64] = {};  // the shared-memory limits belong to a device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 64 || !set[dev]) {
+      e = cudaFuncSetAttribute(prefix_kernel<HD, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(rows_kernel<HD, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 rows_smem(kWarps, HD, 8 + num_sms()));
+      if (e != cudaSuccess) return e;
+      if (dev < 64) set[dev] = true;
+    }
+  }
   if (p.use_prefix) {
     prefix_geometry(p.B * p.gq, p.hkv, p.P, C::kSlots, num_sms(), &p);
     p.part = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(p.part + part_rows(p, C::kSlots) * HD);
     PrefixMaps maps;
-    cudaError_t e = encode_map(&maps.k, p.pk, HD, p.P, (int)p.prefix_cap, p.hkv);
+    e = encode_map(&maps.k, p.pk, HD, p.P, (int)p.prefix_cap, p.hkv);
     if (e == cudaSuccess) e = encode_map(&maps.v, p.pv, HD, p.P, (int)p.prefix_cap, p.hkv);
     if (e != cudaSuccess) return e;
-    static std::mutex mu;
-    static bool set[64] = {};  // the shared-memory limit belongs to a device
-    int dev = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    {
-      std::lock_guard<std::mutex> lock(mu);
-      if (dev >= 64 || !set[dev]) {
-        e = cudaFuncSetAttribute(prefix_kernel<HD, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-        if (e != cudaSuccess) return e;
-        if (dev < 64) set[dev] = true;
-      }
-    }
-    prefix_kernel<HD, TERMS><<<p.n_cta, C::kThreads, C::kSmem, s>>>(p, maps);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t pc;
+    memset(&pc, 0, sizeof(pc));
+    pc.gridDim = dim3((unsigned)p.n_cta);
+    pc.blockDim = dim3(C::kThreads);
+    pc.dynamicSmemBytes = C::kSmem;
+    pc.stream = s;
+    cudaLaunchAttribute pa[1];
+    pa[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pa[0].val.programmaticStreamSerializationAllowed = 1;
+    pc.attrs = pa;
+    pc.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&pc, prefix_kernel<HD, TERMS>, p, maps)) != cudaSuccess) return e;
   }
+  // Warps of a pair (sequence, kv head): as many as run at once (8 an SM, by their rings), and enough for a warp to take 1024
+  // keys at most of a full cache; where 4 are too few, blocks in a cluster.
+  const long long pairs = (long long)p.B * p.hkv * p.hblocks, keys = p.max_seq + (p.use_prefix ? 0 : p.P);
+  int warps = 1;
+  while (warps < kWarps * 8 && warps * 16 < keys && (pairs * warps * 2 <= 8LL * num_sms() || warps * 1024 < keys)) warps *= 2;
+  p.row_cluster = warps > kWarps ? warps / kWarps : 1;
+  warps /= p.row_cluster;
+  p.parts = 8 + (p.use_prefix ? p.n_cta : 0);  // warps or blocks of a cluster: 8 at most
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)(p.B * p.hkv * p.hblocks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)kWarps * kHeads * HD * 4;
+  cfg.gridDim = dim3((unsigned)(pairs * p.row_cluster));
+  cfg.blockDim = dim3((unsigned)(32 * warps));
+  cfg.dynamicSmemBytes = (size_t)rows_smem(warps, HD, p.parts);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (p.use_prefix) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (p.row_cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = (unsigned)p.row_cluster;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = p.use_prefix ? 1 : 0;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, rows_kernel<HD, TERMS>, p);
 }
 

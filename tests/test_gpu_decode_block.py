@@ -395,9 +395,28 @@ def test_shared_prefix_attention_every_end(spd, dtype, P):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("P", [64, 127, 128, 129, 191, 255, 256, 257, 383, 385])
+def test_shared_prefix_attention_every_end_wide_batch(spd, dtype, P):
+    """The same ends where the batch is wide enough for the tensor cores (see the bytes that prefix_pays counts)."""
+    hd = 128 if P < 200 else 64
+    assert spd.shared_prefix_attention_workspace_bytes(128, 16, 16, hd, P) > 16
+    _check_attn(spd, 128, P, 20, 16, 16, hd, dtype, extra=P % 5)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,P,hq,hkv,hd", [(128, 300, 16, 8, 128), (129, 300, 16, 8, 128), (300, 500, 4, 4, 64), (37, 1500, 28, 4, 128),
+                                           (520, 1000, 14, 2, 64), (3, 40000, 8, 1, 128), (16, 9000, 40, 2, 64)])
+def test_shared_prefix_attention_tiles_and_runs(spd, dtype, B, P, hq, hkv, hd):
+    """Rows that fill, just pass and straddle tiles of 128 and pairs of them; runs of chunks that cross from one tile to the next."""
+    assert spd.shared_prefix_attention_workspace_bytes(B, hq, hkv, hd, P) > 16
+    _check_attn(spd, B, P, 9, hq, hkv, hd, dtype, extra=1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_shared_prefix_attention_large_scores(spd, dtype):
     """Scores of +-100: one key carries the row; earlier parts are scaled away."""
     _check_attn(spd, 9, 700, 50, 8, 2, 128, dtype, std=30.0)
+    _check_attn(spd, 150, 700, 50, 8, 2, 128, dtype, std=30.0)
 
 
 def test_shared_prefix_attention_empty_rows_and_bad_lengths(spd):
@@ -440,9 +459,31 @@ def test_shared_prefix_attention_nan_keys_stay_in_their_rows(spd):
     assert nan.cpu().tolist() == [[False, False, True, True], [True, True, True, True], [False, False, True, True]]
 
 
-def test_shared_prefix_attention_repeats_bit_for_bit_and_on_two_streams(spd):
+def test_shared_prefix_attention_nan_and_infinite_keys_wide_batch(spd):
+    """The same through the tensor cores; an infinite score leaves no other row touched."""
+    g = _g(15)
+    B, P, hq, hkv, hd = 140, 700, 4, 2, 128
+    q = _rn(g, B, hq, hd, dtype=BF16)
+    pk, pv = _rn(g, hkv, P, hd, dtype=BF16), _rn(g, hkv, P, hd, dtype=BF16)
+    kc, vc = _rn(g, B, hkv, 20, hd, dtype=BF16), _rn(g, B, hkv, 20, hd, dtype=BF16)
+    lens = torch.full((B,), 20, dtype=torch.int32, device="cuda")
+    assert spd.shared_prefix_attention_workspace_bytes(B, hq, hkv, hd, P) > 16
+    want, _ = _run_attn(spd, q, pk, pv, P, kc, vc, lens)
+    pk[1, 150, 0] = float("nan")
+    q[7, 0] = float("nan")
+    q[9, 1, 3] = float("inf")
+    out, lse = _run_attn(spd, q, pk, pv, P, kc, vc, lens)
+    assert torch.isnan(out[:, 2:]).all() and torch.isnan(lse[:, 2:]).all()
+    bad = torch.zeros(B, 2, dtype=torch.bool, device="cuda")
+    bad[7, 0] = bad[9, 1] = True
+    assert torch.equal(torch.isnan(out[:, :2]).any(2), bad)
+    assert torch.equal(out[:, :2][~bad], want[:, :2][~bad])
+
+
+@pytest.mark.parametrize("B,P", [(24, 3000), (24, 300)])
+def test_shared_prefix_attention_repeats_bit_for_bit_and_on_two_streams(spd, B, P):
     g = _g(13)
-    B, P, hq, hkv, hd = 24, 3000, 16, 4, 128
+    hq, hkv, hd = 16, 4, 128
     q = _rn(g, B, hq, hd, dtype=BF16)
     pk, pv = _rn(g, hkv, P, hd, dtype=BF16), _rn(g, hkv, P, hd, dtype=BF16)
     kc, vc = _rn(g, B, hkv, 40, hd, dtype=BF16), _rn(g, B, hkv, 40, hd, dtype=BF16)
