@@ -479,58 +479,52 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
 # the attention block of a decode step for many continuations of one prompt
 # ---------------------------------------------------------------------------
 _DT = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_I32, _BF16 = torch.int32, torch.bfloat16
+# the short forms of torch.cuda.current_stream(device).cuda_stream and torch.cuda.current_device()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _bad(msg: str) -> "SpdError":
     return SpdError(-1, msg)
 
 
-def _call(fn, args, device: int, stream) -> None:
-    """Runs a C entry on the tensors' device, on `stream` or else torch's current stream there."""
-    if stream is not None:
-        s = _stream_handle(stream)
-    elif _raw_stream is not None:
-        s = _raw_stream(device)
-    else:
-        s = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device:
-        rc = fn(*args, s)
+def _stream_of(device: int, stream) -> int:
+    """`stream`, or else torch's current stream on the device."""
+    return _raw_stream(device) if stream is None else _stream_handle(stream)
+
+
+def _call(fn, device: int, args) -> None:
+    """Runs a C entry with the tensors' device current."""
+    if _current_device() == device:
+        rc = fn(*args)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, s)
+            rc = fn(*args)
     if rc:
         _check(rc)
 
 
-def _device(ts) -> int:
-    """Ordinal of the one GPU that all of `ts` live on."""
-    d = -1
+def _same_device(dev: int, *ts) -> None:
+    if dev < 0:
+        raise _bad("tensor must live on the GPU")
     for t in ts:
-        if t is None:
-            continue
-        i = t.get_device()
-        if i < 0:
-            raise _bad("tensor must live on the GPU")
-        if d < 0:
-            d = i
-        elif i != d:
-            raise _bad("tensors live on different GPUs")
-    return d
+        if t.get_device() != dev:
+            raise _bad("tensors must live on one GPU")
 
 
-def _heads(name: str, t: torch.Tensor, hd: int) -> int:
+def _tokens(name: str, shape, stride, hd: int) -> int:
     """Token stride of a [T, heads, hd] tensor whose tokens are contiguous."""
-    if t.dim() != 3 or t.size(2) != hd:
+    if len(shape) != 3 or shape[2] != hd:
         raise _bad(f"{name} must be [T, heads, {hd}]")
-    if t.size(0) and t.size(1) and (t.stride(2) != 1 or (t.size(1) > 1 and t.stride(1) != hd)):
+    T, heads, _ = shape
+    if T and heads and (stride[2] != 1 or (stride[1] != hd and heads > 1)):
         raise _bad(f"{name}: the heads of a token must be contiguous")
-    # the stride of a dimension of size 1 says nothing
-    return t.stride(0) if t.size(0) > 1 else t.size(1) * hd
+    return stride[0] if T > 1 else heads * hd  # the stride of a dimension of size 1 says nothing
 
 
 def _ints(name: str, t: torch.Tensor, n: int) -> int:
-    if t.dtype != torch.int32 or t.dim() != 1 or t.size(0) != n or not t.is_contiguous():
+    if t.dtype is not _I32 or t.shape != (n,) or not t.is_contiguous():
         raise _bad(f"{name} must be a contiguous int32 tensor of {n} elements")
     return t.data_ptr()
 
@@ -564,41 +558,47 @@ def rope_append(rope: Rope, q: Optional[torch.Tensor], q_out: Optional[torch.Ten
     q, k, v share a dtype (fp32 or bf16) and may be parts of one fused row (any token stride); the caches are fp32 or
     bf16.  Without k only q is rotated; q may be None with k given.  ``stream``: None is torch's current stream."""
     hd = rope.head_dim
-    dev = _device((q, q_out, pos, k, v, k_cache, v_cache, slot, seq))
-    T = pos.numel()
+    if pos.dtype is not _I32 or pos.dim() != 1 or not pos.is_contiguous():
+        raise _bad("pos must be a contiguous int32 vector")
+    dev, T = pos.get_device(), pos.numel()
     qp = qo = kp = vp = kcp = vcp = sp = sqp = None
     qs = qos = ks = vs = hq = hkv = n_seqs = max_seq = 0
-    x = q if q is not None else k
-    if x is None:
-        raise _bad("q and k are both None")
-    if x.dtype not in _DT:
-        raise _bad("q, k and v must be fp32 or bf16")
-    cdt = x.dtype
+    dt = (q if q is not None else k).dtype if q is not None or k is not None else None
+    if dt not in _DT:
+        raise _bad("q or k is needed, in fp32 or bf16")
+    cdt = dt
     if q is not None:
-        if q_out is None or q_out.shape != q.shape or q_out.dtype != q.dtype or q.size(0) != T:
+        if q_out is None:
+            raise _bad("q needs q_out")
+        shape = q.shape
+        if q_out.shape != shape or q_out.dtype is not dt or shape[0] != T:
             raise _bad("q_out must have q's shape and dtype, and pos one entry a token")
-        qs, qos, hq, qp, qo = _heads("q", q, hd), _heads("q_out", q_out, hd), q.size(1), q.data_ptr(), q_out.data_ptr()
+        _same_device(dev, q, q_out)
+        qs, qos, hq = _tokens("q", shape, q.stride(), hd), _tokens("q_out", shape, q_out.stride(), hd), shape[1]
+        qp, qo = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise _bad("q_out without q")
     if k is not None:
         if v is None or k_cache is None or v_cache is None or slot is None:
             raise _bad("k needs v, k_cache, v_cache and slot")
-        if k.dtype != x.dtype or v.dtype != x.dtype or v.shape != k.shape or k.size(0) != T:
+        shape, cdt, cshape = k.shape, k_cache.dtype, k_cache.shape
+        if k.dtype is not dt or v.dtype is not dt or v.shape != shape or shape[0] != T:
             raise _bad("k and v must have q's dtype and tokens, and one shape")
-        ks, vs, hkv, kp, vp = _heads("k", k, hd), _heads("v", v, hd), k.size(1), k.data_ptr(), v.data_ptr()
-        shape = k_cache.shape
-        cdt = k_cache.dtype
-        if (len(shape) not in (3, 4) or shape[-3] != hkv or shape[-1] != hd or v_cache.shape != shape or v_cache.dtype != cdt
+        _same_device(dev, k, v, k_cache, v_cache, slot)
+        ks, vs, hkv = _tokens("k", shape, k.stride(), hd), _tokens("v", shape, v.stride(), hd), shape[1]
+        nd = len(cshape)
+        if (nd not in (3, 4) or cshape[nd - 3] != hkv or cshape[nd - 1] != hd or v_cache.shape != cshape or v_cache.dtype is not cdt
                 or cdt not in _DT or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
             raise _bad("caches must be contiguous [n_seqs, Hkv, max_seq, hd] or [Hkv, max_seq, hd] in fp32 or bf16")
-        n_seqs, max_seq = (shape[0] if len(shape) == 4 else 1), shape[-2]
-        kcp, vcp, sp = k_cache.data_ptr(), v_cache.data_ptr(), _ints("slot", slot, T)
+        n_seqs, max_seq = (cshape[0] if nd == 4 else 1), cshape[nd - 2]
+        kp, vp, kcp, vcp, sp = k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ints("slot", slot, T)
         if seq is not None:
+            _same_device(dev, seq)
             sqp = _ints("seq", seq, T)
     elif v is not None or k_cache is not None or v_cache is not None or slot is not None or seq is not None:
         raise _bad("v, the caches, slot and seq belong to k")
-    _call(lib().spd_rope_append, (rope._at, qp, qs, qo, qos, kp, ks, vp, vs, _DT[x.dtype], _ints("pos", pos, T), T, hq, hkv,
-                                  kcp, vcp, _DT[cdt], sp, sqp, n_seqs, max_seq), dev, stream)
+    _call(lib().spd_rope_append, dev, (rope._at, qp, qs, qo, qos, kp, ks, vp, vs, _DT[dt], pos.data_ptr(), T, hq, hkv, kcp, vcp,
+                                       _DT[cdt], sp, sqp, n_seqs, max_seq, _stream_of(dev, stream)))
 
 
 class Q4Matrix:
@@ -617,14 +617,15 @@ def q4_quantize(w: torch.Tensor, group: int = 128, symmetric: bool = True, scale
     if w.dim() != 2 or w.dtype not in _DT or not w.is_contiguous() or scale_dtype not in _DT:
         raise _bad("w must be a contiguous fp32 or bf16 matrix, scale_dtype fp32 or bf16")
     rows, cols = w.shape
-    dev = _device((w,))
+    dev = w.get_device()
+    _same_device(dev)
     if group not in (32, 64, 128) or cols % group:
         raise _bad("group must be 32, 64 or 128 and divide the columns")
     codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device=w.device)
     scales = torch.empty(rows, cols // group, dtype=scale_dtype, device=w.device)
     zeros = None if symmetric else torch.empty(rows, cols // group, dtype=torch.uint8, device=w.device)
-    _call(lib().spd_q4_quantize, (w.data_ptr(), _DT[w.dtype], rows, cols, group, _DT[scale_dtype], codes.data_ptr(),
-                                  scales.data_ptr(), None if zeros is None else zeros.data_ptr()), dev, stream)
+    _call(lib().spd_q4_quantize, dev, (w.data_ptr(), _DT[w.dtype], rows, cols, group, _DT[scale_dtype], codes.data_ptr(),
+                                       scales.data_ptr(), None if zeros is None else zeros.data_ptr(), _stream_of(dev, stream)))
     return codes, scales, zeros
 
 
@@ -635,7 +636,8 @@ def q4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Ten
         raise _bad("codes must be contiguous uint8 [rows, cols/2], scales fp32 or bf16 [rows, cols/group]")
     if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape or not zeros.is_contiguous()):
         raise _bad("zeros must be contiguous uint8 in the scales' shape")
-    dev = _device((codes, scales, zeros))
+    dev = codes.get_device()
+    _same_device(dev, scales, *(() if zeros is None else (zeros,)))
     rows, cols = codes.size(0), codes.size(1) * 2
     group = cols // scales.size(1)
     if group not in (32, 64, 128) or group * scales.size(1) != cols:
@@ -644,8 +646,8 @@ def q4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Ten
     if n == 0:
         raise _bad("matrix sizes out of range")
     packed = torch.empty(n, dtype=torch.uint8, device=codes.device)
-    _call(lib().spd_q4_pack, (codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(), rows, cols, group,
-                              _DT[scales.dtype], packed.data_ptr(), n), dev, stream)
+    _call(lib().spd_q4_pack, dev, (codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(), rows, cols,
+                                   group, _DT[scales.dtype], packed.data_ptr(), n, _stream_of(dev, stream)))
     return Q4Matrix(packed, rows, cols, group, scales.dtype, zeros is not None)
 
 
@@ -659,35 +661,35 @@ def q4_gemv(Ws: Sequence[Q4Matrix], xs: Sequence[torch.Tensor], ys: Sequence[tor
     if G < 1 or G > 34 or len(xs) != G or len(ys) != G:
         raise _bad("q4_gemv takes 1 to 34 matrices, with a vector and an output each")
     kind, dev, x0 = Ws[0]._kind, Ws[0]._dev, xs[0]
-    cols, dt, nd = kind[0], x0.dtype, x0.dim()
-    M = 1 if nd == 1 else x0.size(0)
+    cols, dt = kind[0], x0.dtype
+    shape = x0.shape
+    nd = len(shape)
     if dt not in _DT or nd not in (1, 2):
         raise _bad("xs must be fp32 or bf16, [M, cols] or [cols]")
-    arr = (spd_q4_group * G)()
-    for g in range(G):
-        W, x, y = Ws[g], xs[g], ys[g]
+    M = 1 if nd == 1 else shape[0]
+    words = []  # the fields of spd_q4_group, 8 bytes each (rows and reserved share one)
+    for W, x, y in zip(Ws, xs, ys):
         if W._kind != kind:
             raise _bad("the matrices of a call share columns, group, scale dtype and zero points")
-        if (x.dtype != dt or y.dtype != dt or x.dim() != nd or y.dim() != nd or x.size(-1) != cols or y.size(-1) != W.rows
-                or x.stride(-1) != 1 or (y.stride(-1) != 1 and W.rows > 1)):
-            raise _bad(f"group {g}: x must be [M, {cols}] and y [M, {W.rows}], one dtype, contiguous rows")
-        if nd == 2 and (x.size(0) != M or y.size(0) != M):
-            raise _bad("all groups take the same number of vectors")
+        sx, sy = x.stride(), y.stride()
+        if x.dtype is not dt or y.dtype is not dt or x.shape != shape or y.shape != (shape[:-1] + (W.rows,)):
+            raise _bad(f"xs must be [M, {cols}] and ys [M, rows of the matrix], in one dtype, with one M")
+        if shape[-1] != cols or sx[-1] != 1 or (sy[-1] != 1 and W.rows > 1):
+            raise _bad(f"x and y rows must be contiguous, x of {cols} columns")
         if x.get_device() != dev or y.get_device() != dev or W._dev != dev:
             raise _bad("tensors must live on one GPU")
-        a = arr[g]
-        a.w, a.x, a.y, a.rows = W._ptr, x.data_ptr(), y.data_ptr(), W.rows
-        if M > 1:
-            a.x_stride, a.y_stride = x.stride(0), y.stride(0)
+        words += (W._ptr, x.data_ptr(), y.data_ptr(), sx[0] if M > 1 else 0, sy[0] if M > 1 else 0, W.rows)
     nw = None
     if norm_weight is not None:
-        if (norm_weight.dtype != torch.float32 or norm_weight.dim() != 1 or norm_weight.numel() != cols or not norm_weight.is_contiguous()
+        if (norm_weight.dtype is not torch.float32 or norm_weight.shape != (cols,) or not norm_weight.is_contiguous()
                 or norm_weight.get_device() != dev):
             raise _bad(f"norm_weight must be a contiguous fp32 vector of {cols} elements on the same GPU")
         nw = norm_weight.data_ptr()
     if M == 0:
         return
-    _call(lib().spd_q4_gemv, (ctypes.addressof(arr), G, M, cols, kind[1], kind[2], kind[3], _DT[dt], nw, eps), dev, stream)
+    arr = (ctypes.c_int64 * len(words))(*words)
+    _call(lib().spd_q4_gemv, dev, (ctypes.addressof(arr), G, M, cols, kind[1], kind[2], kind[3], _DT[dt], nw, eps,
+                                   _stream_of(dev, stream)))
 
 
 def shared_prefix_attention_workspace_bytes(B: int, n_heads: int, n_kv_heads: int, head_dim: int, prefix_len: int) -> int:
@@ -703,39 +705,45 @@ def shared_prefix_attention(q: torch.Tensor, prefix_k: Optional[torch.Tensor], p
     q, out [B, Hq, hd] (fp32 or bf16); prefix_k, prefix_v [Hkv, prefix_cap, hd] bf16, of which the first prefix_len rows
     count; k_cache, v_cache [B, Hkv, max_seq, hd] bf16 with lens int32 [B] rows each (None: no own keys); lse fp32 [B, Hq]
     or None.  A sequence without keys gets 0 and lse -inf, one with lens out of range NaN."""
-    if q.dim() != 3 or q.dtype not in _DT or out.shape != q.shape or out.dtype != q.dtype:
+    shape, dt = q.shape, q.dtype
+    if len(shape) != 3 or dt not in _DT or out.shape != shape or out.dtype is not dt:
         raise _bad("q and out must be [B, Hq, hd] in fp32 or bf16")
     if not q.is_contiguous() or not out.is_contiguous() or not workspace.is_contiguous():
         raise _bad("q, out and the workspace must be contiguous")
-    dev = _device((q, prefix_k, prefix_v, k_cache, v_cache, lens, out, workspace, lse))
-    B, hq, hd = q.shape
-    hkv = 0
+    dev = q.get_device()
+    _same_device(dev, out, workspace)
+    B, hq, hd = shape
     pkp = pvp = kcp = vcp = lp = ep = None
-    cap = max_seq = 0
+    hkv = cap = max_seq = 0
     if prefix_k is not None:
-        if (prefix_v is None or prefix_k.dim() != 3 or prefix_k.dtype != torch.bfloat16 or prefix_k.size(2) != hd
-                or prefix_v.shape != prefix_k.shape or prefix_v.dtype != torch.bfloat16 or not prefix_k.is_contiguous()
-                or not prefix_v.is_contiguous()):
+        ks = prefix_k.shape
+        if (prefix_v is None or len(ks) != 3 or ks[2] != hd or prefix_v.shape != ks or prefix_k.dtype is not _BF16
+                or prefix_v.dtype is not _BF16 or not prefix_k.is_contiguous() or not prefix_v.is_contiguous()):
             raise _bad(f"prefix_k and prefix_v must be contiguous bf16 [Hkv, prefix_cap, {hd}]")
-        hkv, cap, pkp, pvp = prefix_k.size(0), prefix_k.size(1), prefix_k.data_ptr(), prefix_v.data_ptr()
+        _same_device(dev, prefix_k, prefix_v)
+        hkv, cap, _ = ks
+        pkp, pvp = prefix_k.data_ptr(), prefix_v.data_ptr()
     elif prefix_v is not None:
         raise _bad("prefix_v without prefix_k")
     if k_cache is not None:
-        if (v_cache is None or lens is None or k_cache.dim() != 4 or k_cache.dtype != torch.bfloat16 or k_cache.size(0) != B
-                or k_cache.size(3) != hd or v_cache.shape != k_cache.shape or v_cache.dtype != torch.bfloat16
-                or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+        ks = k_cache.shape
+        if (v_cache is None or lens is None or len(ks) != 4 or ks[0] != B or ks[3] != hd or v_cache.shape != ks
+                or k_cache.dtype is not _BF16 or v_cache.dtype is not _BF16 or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
             raise _bad(f"k_cache and v_cache must be contiguous bf16 [{B}, Hkv, max_seq, {hd}], with lens")
-        if hkv and k_cache.size(1) != hkv:
+        if hkv and ks[1] != hkv:
             raise _bad("the prefix and the caches differ in kv heads")
-        hkv, max_seq, kcp, vcp, lp = k_cache.size(1), k_cache.size(2), k_cache.data_ptr(), v_cache.data_ptr(), _ints("lens", lens, B)
+        _same_device(dev, k_cache, v_cache, lens)
+        hkv, max_seq = ks[1], ks[2]
+        kcp, vcp, lp = k_cache.data_ptr(), v_cache.data_ptr(), _ints("lens", lens, B)
     elif v_cache is not None or lens is not None:
         raise _bad("v_cache and lens belong to k_cache")
     if not hkv:
         raise _bad("neither a prefix nor caches")
     if lse is not None:
-        if lse.dtype != torch.float32 or lse.shape != (B, hq) or not lse.is_contiguous():
+        if lse.dtype is not torch.float32 or lse.shape != (B, hq) or not lse.is_contiguous():
             raise _bad("lse must be a contiguous fp32 [B, Hq]")
+        _same_device(dev, lse)
         ep = lse.data_ptr()
-    _call(lib().spd_shared_prefix_attention, (q.data_ptr(), _DT[q.dtype], pkp, pvp, prefix_len, cap, kcp, vcp, lp, max_seq, B, hq, hkv,
-                                              hd, out.data_ptr(), ep, workspace.data_ptr(),
-                                              workspace.numel() * workspace.element_size()), dev, stream)
+    _call(lib().spd_shared_prefix_attention, dev, (q.data_ptr(), _DT[dt], pkp, pvp, prefix_len, cap, kcp, vcp, lp, max_seq, B, hq, hkv,
+                                                   hd, out.data_ptr(), ep, workspace.data_ptr(),
+                                                   workspace.numel() * workspace.element_size(), _stream_of(dev, stream)))

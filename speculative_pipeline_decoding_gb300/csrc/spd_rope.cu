@@ -9,9 +9,10 @@
 // then go through sincospif.
 //
 // Bound by memory: every element is read once and written once (bf16, 8192 tokens of 32 + 2 x 8 heads x 128: 201 MB).
-// A block takes whole tokens, so that the r/2 cosines and sines of a token are formed once, by its first threads, and
-// serve all heads from shared memory; a thread's loads are issued before that.  Blocks are persistent over tokens: a
-// thread reads its frequency once.
+// A warp takes a token, or a share of its heads where there are few tokens.  A lane keeps its place within the heads (16
+// bytes of each side of its pairs), so that it needs the cosines and sines of the same pairs for all heads, in registers:
+// they are formed once, spread over the lanes, and handed round through the warp's own shared memory.  No block barrier, and
+// four heads' loads under way before the first is used.
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -21,12 +22,14 @@
 namespace spd {
 namespace rope {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128, kScalarThreads = 256;
+constexpr int kSteps = 4;  // steps of a warp whose loads are under way together
 
 struct Params {
   uint64_t turns[SPD_ROPE_MAX_PAIRS];
   float mscale;
   int rot, hd, hq, hkv, T;
+  int share;  // warps of a token
   const void *q, *k, *v;
   long long qs, ks, vs, qos;
   void *qo, *kc, *vc;
@@ -44,12 +47,6 @@ __device__ __forceinline__ void turn(float& a, float& b, float2 c) {
 template <typename T, int N> struct alignas(sizeof(T) * N <= 16 ? sizeof(T) * N : 16) Pack { T v[N]; };
 
 template <typename T, int N>
-__device__ __forceinline__ void load_f(const T* p, float* f) {
-  const Pack<T, N> x = *reinterpret_cast<const Pack<T, N>*>(p);
-#pragma unroll
-  for (int i = 0; i < N; ++i) f[i] = WTraits<T>::to_f(x.v[i]);
-}
-template <typename T, int N>
 __device__ __forceinline__ void store_f(T* p, const float* f) {
   Pack<T, N> x;
 #pragma unroll
@@ -57,104 +54,167 @@ __device__ __forceinline__ void store_f(T* p, const float* f) {
   *reinterpret_cast<Pack<T, N>*>(p) = x;
 }
 
-// A unit is 2 * VE elements of one head: VE pairs while inside the rotated part.  In the half layout its two vectors of
-// VE elements lie r/2 apart; elsewhere they are neighbours.  VE = 16 bytes of X, or 1 where strides, addresses or r/2 do
-// not allow whole vectors.
-template <typename X, typename C, int VE, bool INTER>
+// Whole vectors of 16 bytes: VE elements of X.  A unit is 2 VE elements of one head, VE pairs while inside the rotated part: in
+// the half layout its two vectors lie r/2 apart, elsewhere they are neighbours.  per_head units a head, 32 / per_head heads
+// a step.
+template <typename X, typename C, bool INTER>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Params p) {
-  __shared__ float2 cs[2][SPD_ROPE_MAX_PAIRS];
-  const int tid = threadIdx.x, half = p.rot >> 1;
-  const int per_head = p.hd / (2 * VE), units = (p.hq + 2 * p.hkv) * per_head;
-  const uint64_t f = tid < half ? p.turns[tid] : 0;
-  constexpr int kB = VE == 1 ? 1 : 4;  // units a thread holds at once
-  int buf = 0;
-  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
-    const int pos = p.pos[t];
-    int slot = -1, sq = 0;
+  constexpr int VE = WTraits<X>::kVec;
+  constexpr int kB = kSteps;
+  __shared__ float2 s_cs[kThreads / 32][SPD_ROPE_MAX_PAIRS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = p.rot >> 1;
+  const int per_head = p.hd / (2 * VE), hps = 32 / per_head, hl = lane / per_head, w = lane - hl * per_head;
+  const int rows = p.hq + 2 * p.hkv, steps = (rows + hps - 1) / hps;
+  float2* trig = s_cs[warp];
+  const bool pairs = w * VE < half;  // of the half layout
+  const int e0 = !INTER && pairs ? w * VE : w * 2 * VE, e1 = !INTER && pairs ? e0 + half : e0 + VE;
+  pdl_wait();
+  pdl_trigger();
+  const long long tasks = (long long)p.T * p.share;
+  for (long long task = (long long)blockIdx.x * (kThreads / 32) + warp; task < tasks; task += (long long)gridDim.x * (kThreads / 32)) {
+    const int t = (int)(task / p.share), part = (int)(task - (long long)t * p.share);
+    const int s0 = part * steps / p.share, s1 = (part + 1) * steps / p.share;
+    const int pos = __ldg(p.pos + t);
+    long long row = -1;  // of the token in the cache, for kv head 0
     if (p.slot) {
-      slot = p.slot[t];
-      sq = p.seq ? p.seq[t] : 0;
+      const int slot = __ldg(p.slot + t), sq = p.seq ? __ldg(p.seq + t) : 0;
+      if (slot >= 0 && slot < p.max_seq && sq >= 0 && sq < p.n_seqs) row = (long long)sq * p.hkv * p.max_seq + slot;
     }
-    const bool keep = slot >= 0 && slot < p.max_seq && sq >= 0 && sq < p.n_seqs;
-    const int n = keep ? units : p.hq * per_head;
-    if (n == 0) continue;  // no barrier for this token: the buffers keep their turn
-    for (int u0 = tid; u0 - tid < n; u0 += kThreads * kB) {
-      float a[kB][VE], b[kB][VE];
-      int e0[kB], e1[kB], head[kB];
+    const X* q = static_cast<const X*>(p.q) + t * p.qs;
+    const X* k = static_cast<const X*>(p.k) + t * p.ks;
+    const X* v = static_cast<const X*>(p.v) + t * p.vs;
+    const int live = row >= 0 ? rows : p.hq;  // padding: queries only
+    float2 cs[VE];
+    for (int s = s0; s < s1; s += kB) {
+      uint4 a[kB], b[kB];
 #pragma unroll
       for (int j = 0; j < kB; ++j) {
-        const int u = u0 + j * kThreads;
-        if (u >= n) continue;
-        head[j] = u / per_head;
-        const int w = u - head[j] * per_head;
-        if (!INTER && w * VE < half) {
-          e0[j] = w * VE;
-          e1[j] = e0[j] + half;
-        } else {
-          e0[j] = w * 2 * VE;
-          e1[j] = e0[j] + VE;
-        }
-        const X* src;
-        if (head[j] < p.hq) src = static_cast<const X*>(p.q) + t * p.qs + (long long)head[j] * p.hd;
-        else if (head[j] < p.hq + p.hkv) src = static_cast<const X*>(p.k) + t * p.ks + (long long)(head[j] - p.hq) * p.hd;
-        else {
-          src = static_cast<const X*>(p.v) + t * p.vs + (long long)(head[j] - p.hq - p.hkv) * p.hd;
-          e0[j] = w * 2 * VE;
-          e1[j] = e0[j] + VE;
-        }
-        load_f<X, VE>(src + e0[j], a[j]);
-        load_f<X, VE>(src + e1[j], b[j]);
+        const int h = (s + j) * hps + hl;
+        if (s + j >= s1 || hl >= hps || h >= live) continue;
+        const X* src = h < p.hq ? q + (long long)h * p.hd
+                                : h < p.hq + p.hkv ? k + (long long)(h - p.hq) * p.hd : v + (long long)(h - p.hq - p.hkv) * p.hd;
+        const bool is_v = h >= p.hq + p.hkv;
+        a[j] = *reinterpret_cast<const uint4*>(src + (is_v ? w * 2 * VE : e0));
+        b[j] = *reinterpret_cast<const uint4*>(src + (is_v ? w * 2 * VE + VE : e1));
       }
-      if (u0 == tid) {
-        if (tid < half) {
-          const uint64_t angle = (uint64_t)(long long)pos * f;
-          float s, c;
-          sincospif((float)(int32_t)(angle >> 32) * 4.656612873077393e-10f, &s, &c);  // 2 x 2^-32
-          cs[buf][tid] = make_float2(c * p.mscale, s * p.mscale);
+      if (s == s0) {
+        __syncwarp();  // the last token's readers
+        for (int i = lane; i < half; i += 32) {
+          const uint64_t angle = (uint64_t)(long long)pos * p.turns[i];
+          float sn, c;
+          sincospif((float)(int32_t)(angle >> 32) * 4.656612873077393e-10f, &sn, &c);  // 2 x 2^-32
+          trig[i] = make_float2(c * p.mscale, sn * p.mscale);
         }
-        __syncthreads();  // the other buffer's readers are past this one before it is written again
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < VE; ++i) cs[i] = w * VE + i < half ? trig[w * VE + i] : make_float2(1.f, 0.f);
       }
 #pragma unroll
       for (int j = 0; j < kB; ++j) {
-        const int u = u0 + j * kThreads;
-        if (u >= n) continue;
-        if (head[j] < p.hq + p.hkv) {
-          if (INTER && VE > 1) {
+        const int h = (s + j) * hps + hl;
+        if (s + j >= s1 || hl >= hps || h >= live) continue;
+        float x[VE], y[VE];
+        WTraits<X>::unpack(a[j], x);
+        WTraits<X>::unpack(b[j], y);
+        const bool is_v = h >= p.hq + p.hkv;
+        if (!is_v) {
+          if (INTER) {
 #pragma unroll
-            for (int i = 0; i + 1 < VE; i += 2) {
-              const int p0 = (e0[j] + i) >> 1, p1 = (e1[j] + i) >> 1;
-              if (p0 < half) turn(a[j][i], a[j][i + 1], cs[buf][p0]);
-              if (p1 < half) turn(b[j][i], b[j][i + 1], cs[buf][p1]);
+            for (int i = 0; i < VE / 2; ++i) {
+              if (w * VE + i < half) turn(x[2 * i], x[2 * i + 1], cs[i]);
+              if (w * VE + VE / 2 + i < half) turn(y[2 * i], y[2 * i + 1], cs[VE / 2 + i]);
             }
-          } else {
-            const int p0 = INTER ? e0[j] >> 1 : e0[j];  // first pair of the unit (a and b are its two sides)
-            if (p0 < half) {
+          } else if (pairs) {
 #pragma unroll
-              for (int i = 0; i < VE; ++i) turn(a[j][i], b[j][i], cs[buf][p0 + i]);
-            }
+            for (int i = 0; i < VE; ++i) turn(x[i], y[i], cs[i]);
           }
         }
-        if (head[j] < p.hq) {
-          X* dst = static_cast<X*>(p.qo) + t * p.qos + (long long)head[j] * p.hd;
-          store_f<X, VE>(dst + e0[j], a[j]);
-          store_f<X, VE>(dst + e1[j], b[j]);
+        const int d0 = is_v ? w * 2 * VE : e0, d1 = is_v ? w * 2 * VE + VE : e1;
+        if (h < p.hq) {
+          X* dst = static_cast<X*>(p.qo) + t * p.qos + (long long)h * p.hd;
+          store_f<X, VE>(dst + d0, x);
+          store_f<X, VE>(dst + d1, y);
         } else {
-          const bool is_v = head[j] >= p.hq + p.hkv;
-          const int h = head[j] - p.hq - (is_v ? p.hkv : 0);
-          C* dst = static_cast<C*>(is_v ? p.vc : p.kc) + (((long long)sq * p.hkv + h) * p.max_seq + slot) * p.hd;
-          store_f<C, VE>(dst + e0[j], a[j]);
-          store_f<C, VE>(dst + e1[j], b[j]);
+          C* dst = static_cast<C*>(is_v ? p.vc : p.kc) + (row + (long long)(h - p.hq - (is_v ? p.hkv : 0)) * p.max_seq) * p.hd;
+          store_f<C, VE>(dst + d0, x);
+          store_f<C, VE>(dst + d1, y);
         }
       }
     }
-    buf ^= 1;
   }
 }
 
-template <typename X, typename C, int VE>
-void launch(const Params& p, bool inter, int grid, cudaStream_t s) {
-  if (inter) rope_kernel<X, C, VE, true><<<grid, kThreads, 0, s>>>(p);
-  else rope_kernel<X, C, VE, false><<<grid, kThreads, 0, s>>>(p);
+// Element by element, for strides, addresses or a half of the rotated part that do not allow whole vectors: a block a token.
+template <typename X, typename C, bool INTER>
+__global__ void __launch_bounds__(kScalarThreads) rope_scalar_kernel(const __grid_constant__ Params p) {
+  __shared__ float2 trig[2][SPD_ROPE_MAX_PAIRS];
+  const int tid = threadIdx.x, half = p.rot >> 1;
+  const int per_head = p.hd / 2, units = (p.hq + 2 * p.hkv) * per_head;
+  int buf = 0;
+  pdl_wait();
+  pdl_trigger();
+  for (int t = blockIdx.x; t < p.T; t += gridDim.x, buf ^= 1) {
+    long long row = -1;
+    if (p.slot) {
+      const int slot = __ldg(p.slot + t), sq = p.seq ? __ldg(p.seq + t) : 0;
+      if (slot >= 0 && slot < p.max_seq && sq >= 0 && sq < p.n_seqs) row = (long long)sq * p.hkv * p.max_seq + slot;
+    }
+    for (int i = tid; i < half; i += kScalarThreads) {
+      const uint64_t angle = (uint64_t)(long long)__ldg(p.pos + t) * p.turns[i];
+      float sn, c;
+      sincospif((float)(int32_t)(angle >> 32) * 4.656612873077393e-10f, &sn, &c);
+      trig[buf][i] = make_float2(c * p.mscale, sn * p.mscale);
+    }
+    __syncthreads();  // the other buffer's readers are past this one before it is written again
+    const int n = row >= 0 ? units : p.hq * per_head;
+    for (int u = tid; u < n; u += kScalarThreads) {
+      const int h = u / per_head, w = u - h * per_head;
+      const bool is_v = h >= p.hq + p.hkv, pairs = !INTER && w < half && !is_v;
+      const int e0 = pairs ? w : 2 * w, e1 = pairs ? w + half : 2 * w + 1;
+      const X* src = h < p.hq ? static_cast<const X*>(p.q) + t * p.qs + (long long)h * p.hd
+                              : is_v ? static_cast<const X*>(p.v) + t * p.vs + (long long)(h - p.hq - p.hkv) * p.hd
+                                     : static_cast<const X*>(p.k) + t * p.ks + (long long)(h - p.hq) * p.hd;
+      float x = WTraits<X>::to_f(src[e0]), y = WTraits<X>::to_f(src[e1]);
+      if (w < half && !is_v) turn(x, y, trig[buf][w]);
+      if (h < p.hq) {
+        X* dst = static_cast<X*>(p.qo) + t * p.qos + (long long)h * p.hd;
+        dst[e0] = WTraits<X>::from_f(x);
+        dst[e1] = WTraits<X>::from_f(y);
+      } else {
+        C* dst = static_cast<C*>(is_v ? p.vc : p.kc) + (row + (long long)(h - p.hq - (is_v ? p.hkv : 0)) * p.max_seq) * p.hd;
+        dst[e0] = WTraits<C>::from_f(x);
+        dst[e1] = WTraits<C>::from_f(y);
+      }
+    }
+  }
+}
+
+template <typename X, typename C>
+cudaError_t launch(Params& p, bool vec, bool inter, cudaStream_t s) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const int sms = num_sms();
+  if (!vec) {
+    cfg.gridDim = dim3((unsigned)(p.T < 8 * sms ? p.T : 8 * sms));
+    cfg.blockDim = dim3(kScalarThreads);
+    return inter ? cudaLaunchKernelEx(&cfg, rope_scalar_kernel<X, C, true>, p) : cudaLaunchKernelEx(&cfg, rope_scalar_kernel<X, C, false>, p);
+  }
+  // shares of a token: kSteps steps each, whose loads are under way together, as far as the GPU's warps (24 an SM) go
+  const int per_head = p.hd / (2 * WTraits<X>::kVec), hps = 32 / per_head, steps = (p.hq + 2 * p.hkv + hps - 1) / hps;
+  const int warps = 24 * sms, wpb = kThreads / 32;
+  const int share = warps / p.T;
+  const int most = (steps + kSteps - 1) / kSteps;
+  p.share = share < 1 ? 1 : share > most ? most : share;
+  const long long blocks = ((long long)p.T * p.share + wpb - 1) / wpb;
+  cfg.gridDim = dim3((unsigned)(blocks < warps / wpb ? blocks : warps / wpb));
+  cfg.blockDim = dim3(kThreads);
+  return inter ? cudaLaunchKernelEx(&cfg, rope_kernel<X, C, true>, p) : cudaLaunchKernelEx(&cfg, rope_kernel<X, C, false>, p);
 }
 
 }  // namespace rope
@@ -240,16 +300,13 @@ extern "C" int spd_rope_append(const spd_rope* rope, const void* q, int64_t q_st
   auto ok = [](const void* ptr, long long stride, int n) { return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && stride % n == 0; };
   if (n_heads) vec = vec && ok(q, q_stride, ve) && ok(q_out, q_out_stride, ve);
   if (n_kv_heads) vec = vec && ok(k, k_stride, ve) && ok(v, v_stride, ve) && ok(k_cache, 0, 1) && ok(v_cache, 0, 1);
-  const int grid = T < 8 * num_sms() ? T : 8 * num_sms();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(cuda_stream);
   cudaGetLastError();
-#define SPD_ROPE_GO(X, C, VE) rope::launch<X, C, VE>(p, inter, grid, s)
-  if (xf && cf) { if (vec) SPD_ROPE_GO(float, float, 4); else SPD_ROPE_GO(float, float, 1); }
-  else if (xf) { if (vec) SPD_ROPE_GO(float, __nv_bfloat16, 4); else SPD_ROPE_GO(float, __nv_bfloat16, 1); }
-  else if (cf) { if (vec) SPD_ROPE_GO(__nv_bfloat16, float, 8); else SPD_ROPE_GO(__nv_bfloat16, float, 1); }
-  else { if (vec) SPD_ROPE_GO(__nv_bfloat16, __nv_bfloat16, 8); else SPD_ROPE_GO(__nv_bfloat16, __nv_bfloat16, 1); }
-#undef SPD_ROPE_GO
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (xf && cf) e = rope::launch<float, float>(p, vec, inter, s);
+  else if (xf) e = rope::launch<float, __nv_bfloat16>(p, vec, inter, s);
+  else if (cf) e = rope::launch<__nv_bfloat16, float>(p, vec, inter, s);
+  else e = rope::launch<__nv_bfloat16, __nv_bfloat16>(p, vec, inter, s);
   if (e != cudaSuccess) {
     char msg[160];
     snprintf(msg, sizeof(msg), "spd_rope_append: launch: %s", cudaGetErrorString(e));
