@@ -523,6 +523,8 @@ __device__ __forceinline__ float4 remote4(const float* p, int rank) {
   return v;
 }
 
+template <int N> struct Int { static constexpr int value = N; };
+
 // Shared memory of the rows kernel: the warps' rings (afterwards O, maxima and sums of the warps), the weights of the parts,
 // the barriers.
 constexpr int kRing = 3;                                       // steps of 16 keys that a warp has under way
@@ -775,96 +777,107 @@ __global__ void __launch_bounds__(kThreads, TERMS == 1 ? 3 : 2) rows_kernel(cons
       }
       return (long long)(first + u) * (NS * kTile) + prow % (NS * kTile);
     };
-    // the first parts of this thread's first output on their way while the weights are formed
-    constexpr int kFirst = 12;
-    float4 early[kFirst];
+    // Weights of the parts: 4 W neighbouring lanes a head, all heads at once.
     {
-      int np;
-      const int h = tid % nh, d = tid / nh * 4;
-      const long long at = prefix_parts(h, &np);
-      const float* src = p.part + at / kTile * (kTile * HD) + d * kTile + at % kTile * 4;
-#pragma unroll
-      for (int x = 0; x < kFirst; ++x)
-        if (x < np && d < HD) early[x] = __ldcg(reinterpret_cast<const float4*>(src + (long long)x * NS * kTile * HD));
-    }
-    // weights of the parts, a warp a head
-    for (int h = warp; h < nh; h += W) {
+      const int L = 4 * W, h = min(tid / L, nh - 1), l0 = tid % L;  // heads that do not exist repeat the last one
       int np;
       const long long at = prefix_parts(h, &np);
       const float2* ml = p.part_ml + at;
       float* wt = s_w + h * p.parts;
+      const int n = nw + np;
+      auto get = [&](int j) {
+        return j < nw ? (CS > 1 ? make_float2(remote(&s_m[h], j), remote(&s_l[h], j)) : make_float2(s_m[j * kHeads + h], s_l[j * kHeads + h]))
+                      : __ldcg(ml + (long long)(j - nw) * NS * kTile);
+      };
       float mx = -INFINITY, lt = 0.f;
-      for (int j0 = 0; j0 < nw + np; j0 += 32) {
-        const int j = j0 + lane;
-        float2 v = make_float2(-INFINITY, 0.f);
-        if (j < nw) v = CS > 1 ? make_float2(remote(&s_m[h], j), remote(&s_l[h], j)) : make_float2(s_m[j * kHeads + h], s_l[j * kHeads + h]);
-        else if (j < nw + np) v = __ldcg(ml + (long long)(j - nw) * NS * kTile);
-        float mn = v.x;
+      for (int j = l0; j < n; j += 4 * L) {
+        float2 v[4];
 #pragma unroll
-        for (int x = 16; x; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
-        mn = fmaxf(mn, mx);
-        const float mu = mn == -INFINITY ? 0.f : mn;
-        lt = lt * ex2(mx - mu) + v.y * ex2(v.x - mu);  // of this lane's parts
+        for (int x = 0; x < 4; ++x) v[x] = j + x * L < n ? get(j + x * L) : make_float2(-INFINITY, 0.f);
+        const float mn = fmaxf(fmaxf(mx, fmaxf(v[0].x, v[1].x)), fmaxf(v[2].x, v[3].x)), mu = mn == -INFINITY ? 0.f : mn;
+        lt *= ex2(mx - mu);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          lt += v[x].y * ex2(v[x].x - mu);
+          if (j + x * L < n && tid / L < nh) wt[j + x * L] = v[x].x;
+        }
         mx = mn;
-        if (j < nw + np) wt[j] = v.x;
       }
-#pragma unroll
-      for (int x = 16; x; x >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, x);
-      const float mu = mx == -INFINITY ? 0.f : mx;
-      for (int j = lane; j < nw + np; j += 32) wt[j] = ex2(wt[j] - mu);
-      if (lane == 0) {
-        s_at[h] = at;
-        s_np[h] = np;
-        s_sum[h] = lt;
-        if (p.lse) p.lse[(long long)b * p.hq + h0 + h] = bad ? NAN : none ? -INFINITY : mx * kLn2 + logf(lt);
+      float ma = mx;
+      for (int x = L >> 1; x; x >>= 1) ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, x));
+      const float mu = ma == -INFINITY ? 0.f : ma;
+      lt *= ex2(mx - mu);
+      for (int x = L >> 1; x; x >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, x);
+      if (tid / L < nh) {
+        for (int j = l0; j < n; j += L) wt[j] = ex2(wt[j] - mu);
+        if (l0 == 0) {
+          s_at[h] = at;
+          s_np[h] = np;
+          s_sum[h] = lt;
+          if (p.lse) p.lse[(long long)b * p.hq + h0 + h] = bad || s_fail ? NAN : none ? -INFINITY : ma * kLn2 + logf(lt);
+        }
       }
     }
     __syncthreads();
-    for (int i = tid; i < nh * (HD / 4); i += blockDim.x) {
-      const int h = i % nh, d = i / nh * 4;  // neighbours: the heads' rows lie side by side in a part
-      const float* wt = s_w + h * p.parts;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      auto add = [&](float w, const float4& v) {
-        combine(y.x, w, v.x); combine(y.y, w, v.y); combine(y.z, w, v.z); combine(y.w, w, v.w);
-      };
-      const int np = s_np[h];
-      const float* src = p.part + s_at[h] / kTile * (kTile * HD) + d * kTile + s_at[h] % kTile * 4;
-      int done = 0;
-      if (i == tid) {
+    // Four elements of a head a thread and item; neighbours take the heads, whose rows lie side by side in a part.  A few
+    // items' loads, or a few parts', are under way together.
+    const int items = nh * (HD / 4);
+    auto outputs = [&](auto n_items, auto n_parts) {
+      constexpr int NI = decltype(n_items)::value, NP = decltype(n_parts)::value;
+      for (int i0 = tid; i0 < items; i0 += NI * blockDim.x) {
+        float4 y[NI];
+        const float* src[NI];
+        const float* wt[NI];
+        int most = 0, np[NI];
 #pragma unroll
-        for (int x = 0; x < kFirst; ++x)
-          if (x < np) add(wt[nw + x], early[x]);
-        done = kFirst;
+        for (int x = 0; x < NI; ++x) {
+          const int i = min(i0 + x * (int)blockDim.x, items - 1), h = i % nh, d = i / nh * 4;
+          y[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+          np[x] = s_np[h];
+          most = max(most, np[x]);
+          wt[x] = s_w + h * p.parts;
+          src[x] = p.part + s_at[h] / kTile * (kTile * HD) + d * kTile + s_at[h] % kTile * 4;
+        }
+        auto add = [&](float4& y, float w, const float4& v) {
+          combine(y.x, w, v.x); combine(y.y, w, v.y); combine(y.z, w, v.z); combine(y.w, w, v.w);
+        };
+        for (int j = 0; j < most; j += NP) {
+          float4 v[NP][NI];
+#pragma unroll
+          for (int k = 0; k < NP; ++k)
+#pragma unroll
+            for (int x = 0; x < NI; ++x)
+              if (j + k < np[x]) v[k][x] = __ldcg(reinterpret_cast<const float4*>(src[x] + (long long)(j + k) * NS * kTile * HD));
+#pragma unroll
+          for (int k = 0; k < NP; ++k)
+#pragma unroll
+            for (int x = 0; x < NI; ++x)
+              if (j + k < np[x]) add(y[x], wt[x][nw + j + k], v[k][x]);
+        }
+#pragma unroll
+        for (int x = 0; x < NI; ++x) {
+          const int i = i0 + x * (int)blockDim.x;
+          if (i >= items) break;
+          const int h = i % nh, d = i / nh * 4;
+          for (int j = 0; j < nw; ++j)
+            add(y[x], wt[x][j], CS > 1 ? remote4(s_o + h * HD + d, j) : *reinterpret_cast<const float4*>(s_o + (j * kHeads + h) * HD + d));
+          const float inv = 1.0f / s_sum[h];
+          float4 o4 = make_float4(y[x].x * inv, y[x].y * inv, y[x].z * inv, y[x].w * inv);
+          if (bad || s_fail) o4 = make_float4(NAN, NAN, NAN, NAN);
+          else if (none) o4 = make_float4(0.f, 0.f, 0.f, 0.f);
+          const long long at = ((long long)b * p.hq + h0 + h) * HD + d;
+          if (TERMS > 1) {
+            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = o4;
+          } else {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(o4.x, o4.y), hi = __floats2bfloat162_rn(o4.z, o4.w);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+          }
+        }
       }
-      for (int j = done; j < np; j += 8) {
-        float4 v[8];
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          if (j + x < np) v[x] = __ldcg(reinterpret_cast<const float4*>(src + (long long)(j + x) * NS * kTile * HD));
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          if (j + x < np) add(wt[nw + j + x], v[x]);
-      }
-      float4 v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)  // nw is at most 8
-        if (j < nw) v[j] = CS > 1 ? remote4(s_o + h * HD + d, j) : *reinterpret_cast<const float4*>(s_o + (j * kHeads + h) * HD + d);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < nw) add(wt[j], v[j]);
-      const float inv = 1.0f / s_sum[h];
-      y.x *= inv; y.y *= inv; y.z *= inv; y.w *= inv;
-      if (bad || s_fail) y = make_float4(NAN, NAN, NAN, NAN);
-      else if (none) y = make_float4(0.f, 0.f, 0.f, 0.f);
-      const long long at = ((long long)b * p.hq + h0 + h) * HD + d;
-      if (TERMS > 1) {
-        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = y;
-      } else {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-      }
-    }
+    };
+    if (items > 2 * (int)blockDim.x) outputs(Int<4>(), Int<4>());
+    else outputs(Int<1>(), Int<12>());
   }
   if (CS > 1) cluster_sync();  // nobody reads this block's shared memory any more
 }
