@@ -52,9 +52,13 @@ struct Params {
   int P, B, hq, hkv, gq, hblocks;
   float scale_log2;  // log2(e) / sqrt(hd)
   // prefix kernel: `units` row tiles (pairs) x nch chunks, cut into n_cta runs; the part of run i for unit u is slot i + u
-  int units_per_kv, units, nch, n_cta;
+  int units_per_kv, units, nch, n_cta, tiles;
   int use_prefix;
-  int row_cluster, parts;  // rows kernel: blocks of a sequence and kv head; most parts of a row
+  int row_cluster;              // rows kernel: blocks of a sequence and kv head
+  // parts kernel: own keys in runs of own_run, own_runs of a sequence; parts: most parts of a row
+  float4* own;
+  float2* own_ml;
+  int own_run, own_runs, parts;
 };
 
 // first chunk of run i
@@ -85,22 +89,33 @@ __device__ __forceinline__ uint32_t take_pair(float& a, float& b) {
 }
 
 
+// The same for probabilities, which are finite or NaN.
+__device__ __forceinline__ uint32_t take_prob(float& a, float& b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+  a -= bf16_lo(u);
+  b -= bf16_hi(u);
+  return u;
+}
+
 // ---------------------------------------------------------------------------------------------
 // prefix kernel
 // ---------------------------------------------------------------------------------------------
 constexpr int kTile = 128;   // rows of a tile, keys of a chunk
+// A block leaves registers (128 a thread) and shared memory for a few warps of the rows kernel beside it, which reads the
+// sequences' own keys meanwhile.
 template <int HD, int TERMS> struct Cfg {
   static constexpr int kSlots = TERMS == 1 ? 2 : 1;              // row tiles of a block
   static constexpr int kTB = HD / 64 * kTile * 128;              // bytes of a 128-row operand
-  static constexpr int kQ = kSlots * TERMS * kTB;                // Q
-  static constexpr int kStages = (227 * 1024 - 2048 - kQ) / kTB > 8 ? 8 : (227 * 1024 - 2048 - kQ) / kTB;
-  static constexpr int kSmem = 1024 + kQ + kStages * kTB;
-  // softmax warps, a copying and a multiplying warp; two tiles: a whole third warpgroup, which gives up registers
-  static constexpr int kThreads = kSlots == 2 ? 384 : 192;
-  // TMEM columns: two tiles: S0 S1 O0 O1, P over S; one tile: S, O, and three P
+  static constexpr int kStages = HD == 128 ? 3 : 6;              // K and V chunks under way
+  static constexpr int smem(int tiles) { return 1024 + (tiles * TERMS + kStages) * kTB; }
+  // softmax warps, a copying and a multiplying warp
+  static constexpr int kThreads = kSlots == 2 ? 320 : 192;
+  static constexpr int kBound = kSlots == 2 ? 512 : 256;         // launch bounds that make 128 registers a thread
+  // TMEM columns: two tiles: S0 S1 O0 O1, P over the second half of S; one tile: S, O, and three P
   static constexpr uint32_t s_col(int i) { return 128u * i; }
   static constexpr uint32_t o_col(int i) { return kSlots == 2 ? 256u + 128u * i : 128u; }
-  static constexpr uint32_t p_col(int i) { return kSlots == 2 ? 128u * i : 256u; }
+  static constexpr uint32_t p_col(int i) { return kSlots == 2 ? 128u * i + 64u : 256u; }
 };
 
 struct PrefixMaps {
@@ -184,13 +199,13 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
 }
 
 template <int HD, int TERMS>
-__global__ void __launch_bounds__(Cfg<HD, TERMS>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<HD, TERMS>::kBound, Cfg<HD, TERMS>::kSlots == 2 ? 1 : 2)
 prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMaps maps) {
   using C = Cfg<HD, TERMS>;
   constexpr int NS = C::kSlots, ST = C::kStages;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sq = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  unsigned char* ring = sq + C::kQ;
+  unsigned char* ring = sq + p.tiles * TERMS * C::kTB;
   __shared__ __align__(8) uint64_t full[ST], empty[ST], q_ready[NS], s_full[NS], p_ready[NS], o_full[NS], s_free[NS], pv_done, drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail_;
@@ -221,7 +236,7 @@ prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMa
   __syncthreads();
   tc::fence_after();
   pdl_wait();
-  pdl_trigger();  // the rows kernel may start its own keys beside this one
+  pdl_trigger();  // what came before the call is done: the parts kernel may start beside this one
   const uint32_t tm = s_tmem;
   const long long total = (long long)p.units * p.nch;
   const long long w0 = run_start(total, p.n_cta, blockIdx.x), w1 = run_start(total, p.n_cta, blockIdx.x + 1);
@@ -240,10 +255,7 @@ prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMa
     return x;
   };
 
-  // Two tiles: 384 threads start with 168 registers each (64,512 in all); 224 for a softmax thread, which holds 128 scores,
-  // and 56 for the others are 2 x 128 x 224 + 128 x 56 = 64,512.
   if (warp >= NS * 4) {
-    if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == kCopyWarp) {
     if ((tid & 31) == 0) {
       int st = 0;
@@ -360,7 +372,6 @@ prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMa
     __syncwarp();
   }
   } else {
-    if (NS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int slot = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t to = tm + C::o_col(slot) + lanes, tp = tm + C::p_col(slot) + lanes;
@@ -372,27 +383,42 @@ prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMa
       if (slot >= x.nt) continue;
       const int row = x.row0 + slot * kTile + r;
       const bool valid = row < rows;
-      {
-        const int b = row / p.gq, h = x.kh * p.gq + row % p.gq;
-        const long long at = ((long long)b * p.hq + h) * HD;
+      {  // Q: 8 elements a thread at a time, neighbours in a row; rows that no query fills are zeros
+        constexpr int per_row = HD / 8, kU = TERMS == 1 ? 8 : 4;
+        const int live = min(kTile, rows - x.row0 - slot * kTile);
         unsigned char* dst = sq + slot * TERMS * C::kTB;
-#pragma unroll (TERMS == 1 ? HD / 8 : 4)
-        for (int e = 0; e < HD; e += 8) {
-          if (TERMS == 1) {
-            const uint4 v = valid ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at + e) : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(dst + swz(r, e)) = v;
-          } else {
-            float f[8] = {};
-            if (valid) {
-              const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at + e);
-              const float4 c = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at + e + 4);
-              f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = c.x; f[5] = c.y; f[6] = c.z; f[7] = c.w;
-            }
+        for (int i0 = r; i0 < kTile * per_row; i0 += kTile * kU) {
+          uint4 v[kU][TERMS == 1 ? 1 : 2];
 #pragma unroll
-            for (int t = 0; t < TERMS; ++t) {
-              uint4 v;
-              v.x = take_pair(f[0], f[1]); v.y = take_pair(f[2], f[3]); v.z = take_pair(f[4], f[5]); v.w = take_pair(f[6], f[7]);
-              *reinterpret_cast<uint4*>(dst + t * C::kTB + swz(r, e)) = v;
+          for (int k = 0; k < kU; ++k) {
+            const int i = i0 + k * kTile, qr = i / per_row, e = i % per_row * 8, gr = x.row0 + slot * kTile + qr;
+#pragma unroll
+            for (int h = 0; h < (TERMS == 1 ? 1 : 2); ++h) v[k][h] = make_uint4(0, 0, 0, 0);
+            if (qr < live) {
+              const long long at = ((long long)(gr / p.gq) * p.hq + x.kh * p.gq + gr % p.gq) * HD + e;
+              if (TERMS == 1) {
+                v[k][0] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at);
+              } else {
+                v[k][0] = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.q) + at);
+                v[k][TERMS == 1 ? 0 : 1] = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.q) + at + 4);
+              }
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kU; ++k) {
+            const int i = i0 + k * kTile, qr = i / per_row, e = i % per_row * 8;
+            if (TERMS == 1) {
+              *reinterpret_cast<uint4*>(dst + swz(qr, e)) = v[k][0];
+            } else {
+              const uint4 lo = v[k][0], hi = v[k][TERMS == 1 ? 0 : 1];
+              float f[8] = {__uint_as_float(lo.x), __uint_as_float(lo.y), __uint_as_float(lo.z), __uint_as_float(lo.w),
+                            __uint_as_float(hi.x), __uint_as_float(hi.y), __uint_as_float(hi.z), __uint_as_float(hi.w)};
+#pragma unroll
+              for (int t = 0; t < TERMS; ++t) {
+                uint4 w;
+                w.x = take_pair(f[0], f[1]); w.y = take_pair(f[2], f[3]); w.z = take_pair(f[4], f[5]); w.w = take_pair(f[6], f[7]);
+                *reinterpret_cast<uint4*>(dst + t * C::kTB + swz(qr, e)) = w;
+              }
             }
           }
         }
@@ -405,22 +431,26 @@ prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMa
         ph_s ^= 1;
         if (!ok) break;
         tc::fence_after();
-        float sv[kTile];
-#pragma unroll
-        for (int j = 0; j < kTile; j += 32) tc::load_rows(tm + C::s_col(slot) + j, warp, reinterpret_cast<uint32_t*>(sv + j));
-        if (NS == 1 && c + 1 < x.c1) {
-          tc::fence_before();
-          mbar_arrive(&s_free[slot]);
-        }
+        // the maximum over both halves of the row; the second half stays in registers, the first is read again
         const int left = p.P - c * kTile;  // keys of this chunk
-        if (left < kTile) {
+        float sv[64], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto half = [&](int j0) {
 #pragma unroll
-          for (int j = 0; j < kTile; ++j)
-            if (j >= left) sv[j] = -INFINITY;
-        }
-        float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+          for (int j = 0; j < 64; j += 32) tc::load_rows(tm + C::s_col(slot) + j0 + j, warp, reinterpret_cast<uint32_t*>(sv + j));
+          if (left < kTile) {
 #pragma unroll
-        for (int j = 4; j < kTile; ++j) mx[j & 3] = fmaxf(mx[j & 3], sv[j]);
+            for (int j = 0; j < 64; ++j)
+              if (j0 + j >= left) sv[j] = -INFINITY;
+          }
+        };
+        auto half_max = [&]() {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], sv[j]);
+        };
+        half(0);
+        half_max();
+        half(64);
+        half_max();
         const float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
         const bool grow = c == x.c0 || mc > m + 8.f;
         float al = 1.f;
@@ -451,17 +481,24 @@ prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMa
         const float mu = m == -INFINITY ? 0.f : m;
         float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < kTile; j += 64) {
+        for (int j = 64; j >= 0; j -= 64) {  // with P over S's second half: the second half first
+          if (j == 0) {
+            half(0);
+            if (NS == 1 && c + 1 < x.c1) {
+              tc::fence_before();
+              mbar_arrive(&s_free[slot]);
+            }
+          }
 #pragma unroll
           for (int t = 0; t < 64; ++t) {
-            sv[j + t] = ex2(fmaf(sv[j + t], p.scale_log2, -mu));
-            ls[t & 3] += sv[j + t];
+            sv[t] = ex2(fmaf(sv[t], p.scale_log2, -mu));
+            ls[t & 3] += sv[t];
           }
 #pragma unroll
           for (int e = 0; e < TERMS; ++e) {
             uint32_t pk[32];
 #pragma unroll
-            for (int t = 0; t < 32; ++t) pk[t] = take_pair(sv[j + 2 * t], sv[j + 2 * t + 1]);
+            for (int t = 0; t < 32; ++t) pk[t] = take_prob(sv[2 * t], sv[2 * t + 1]);
             tm_st32(tp + e * 64 + j / 2, pk);
           }
         }
@@ -502,128 +539,50 @@ prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMa
 }
 
 
-// The sum over the cluster's blocks goes through their shared memory.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t remote_addr(const void* p, int rank) {  // the same place in another block of the cluster
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ float remote(const float* p, int rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote_addr(p, rank)) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 remote4(const float* p, int rank) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(remote_addr(p, rank)) : "memory");
-  return v;
-}
-
-template <int N> struct Int { static constexpr int value = N; };
-
-// Shared memory of the rows kernel: the warps' rings (afterwards O, maxima and sums of the warps), the weights of the parts,
-// the barriers.
+// ---------------------------------------------------------------------------------------------
+// the sequences' own keys: a warp's work
+// ---------------------------------------------------------------------------------------------
 constexpr int kRing = 3;                                       // steps of 16 keys that a warp has under way
 constexpr int stage_bytes(int hd) { return 2 * 16 * hd * 2; }  // K and V
-__host__ __device__ constexpr int rows_smem(int warps, int hd, int parts) {
-  return warps * kRing * stage_bytes(hd) + (kHeads * parts * 4 + 7) / 8 * 8 + warps * kRing * 8;
-}
 
-template <int HD, int TERMS>
-__global__ void __launch_bounds__(kThreads, TERMS == 1 ? 3 : 2) rows_kernel(const __grid_constant__ Params p) {
-  constexpr int KI = HD / 32;  // 16-byte pieces of a key a lane reads
-  constexpr int NS = Cfg<HD, TERMS>::kSlots;
-  extern __shared__ __align__(128) unsigned char smem[];
-  const int W = blockDim.x >> 5;
-  float* s_o = reinterpret_cast<float*>(smem);  // [warp][head][HD], over the rings
-  float* s_m = s_o + W * kHeads * HD;           // [warp][head]
-  float* s_l = s_m + W * kHeads;                // [warp][head]
-  float* s_w = reinterpret_cast<float*>(smem + W * kRing * stage_bytes(HD));  // [head][part]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + rows_smem(W, HD, p.parts) - W * kRing * 8);
-  static_assert(kRing * stage_bytes(HD) >= kHeads * (HD + 2) * 4, "a warp's sums fit over its ring");
-  __shared__ float s_sum[kHeads];
-  __shared__ int s_fail;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int CS = p.row_cluster, rank = blockIdx.x % CS, pair = blockIdx.x / CS;
-  const int hb = pair % p.hblocks, kh = pair / p.hblocks % p.hkv, b = pair / p.hblocks / p.hkv;
-  const int h0 = kh * p.gq + hb * kHeads, nh = min(kHeads, p.gq - hb * kHeads);
-  unsigned char* ring = smem + warp * kRing * stage_bytes(HD);
-  uint64_t* bar = bars + warp * kRing;
-  if (lane == 0) {
-    for (int i = 0; i < kRing; ++i) mbar_init(&bar[i], 1);
-    fence_mbar_init();
-  }
-  if (tid == 0) s_fail = 0;
-  const int len = p.max_seq > 0 ? p.lens[b] : 0;
-  const bool bad = len < 0 || len > p.max_seq;
-  const int P = p.use_prefix ? 0 : p.P;  // prefix keys that this kernel reads itself
-  const int nkeys = bad ? 0 : P + len;
-  const int key_step = CS * W * 16;
-  int key0 = (rank * W + warp) * 16;
-  const __nv_bfloat16* own_k = p.kc + ((long long)b * p.hkv + kh) * p.max_seq * HD;
-  const __nv_bfloat16* own_v = p.vc + ((long long)b * p.hkv + kh) * p.max_seq * HD;
-  const __nv_bfloat16* pre_k = p.pk + (long long)kh * p.prefix_cap * HD;
-  const __nv_bfloat16* pre_v = p.pv + (long long)kh * p.prefix_cap * HD;
-  // the rows of 16 keys from k0, those that exist, into a stage: K [16][HD], V [16][HD]
-  const uint64_t pol = l2_evict_first_policy();
-  auto fetch = [&](int st, int k0) {  // lane 0
-    unsigned char* dst = ring + st * stage_bytes(HD);
-    const int n = min(16, nkeys - k0), a = max(0, min(n, P - k0));  // a of them in the prefix
-    mbar_arrive_expect_tx(&bar[st], (uint32_t)n * HD * 4);
-    if (a > 0) {
-      bulk_g2s(dst, pre_k + (long long)k0 * HD, a * HD * 2, &bar[st], pol);
-      bulk_g2s(dst + 16 * HD * 2, pre_v + (long long)k0 * HD, a * HD * 2, &bar[st], pol);
-    }
-    if (a < n) {
-      const long long at = (long long)(k0 + a - P) * HD;
-      bulk_g2s(dst + a * HD * 2, own_k + at, (n - a) * HD * 2, &bar[st], pol);
-      bulk_g2s(dst + (16 + a) * HD * 2, own_v + at, (n - a) * HD * 2, &bar[st], pol);
-    }
-  };
-  if (lane == 0)
-    for (int i = 0; i < kRing; ++i)
-      if (key0 + i * key_step < nkeys) fetch(i, key0 + i * key_step);
-  // Q^T as the second operand: head g, elements 32 i + 8 t + 4 s + {0, 1}, {2, 3}
-  uint32_t qb[TERMS][KI][2][2];
-#pragma unroll
-  for (int i = 0; i < KI; ++i) {
-    const long long at = ((long long)b * p.hq + h0 + min(g, nh - 1)) * HD + 32 * i + 8 * t;
-    float x[8];
-    if (TERMS > 1) {
-      const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at);
-      const float4 c = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at + 4);
-      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = c.x; x[5] = c.y; x[6] = c.z; x[7] = c.w;
-#pragma unroll
-      for (int e = 0; e < TERMS; ++e)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          qb[e][i][s][0] = take_pair(x[4 * s], x[4 * s + 1]);
-          qb[e][i][s][1] = take_pair(x[4 * s + 2], x[4 * s + 3]);
-        }
-    } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at);
-      qb[0][i][0][0] = a.x; qb[0][i][0][1] = a.y; qb[0][i][1][0] = a.z; qb[0][i][1][1] = a.w;
-    }
-  }
-  float o[HD / 16][4];
-#pragma unroll
-  for (int e = 0; e < HD / 16; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // heads 2 t, 2 t + 1
+// Up to 8 query heads of a kv head against keys in steps of 16.
+template <int HD, int TERMS> struct Rows {
+  static constexpr int KI = HD / 32;  // 16-byte pieces of a key a lane reads
+  uint32_t qb[TERMS][KI][2][2];       // Q^T, the second operand: head g, elements 32 i + 8 t + 4 s + {0, 1}, {2, 3}
+  float o[HD / 16][4], m[2], l[2];    // O^T; maximum and this lane's share of the sum of heads 2 t, 2 t + 1
 
-  __syncwarp();  // the barriers are set up
-  bool ok = true;
-  int st = 0;
-  uint32_t ph = 0;
-  for (; key0 < nkeys; key0 += key_step) {
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[st], ph)) != 0;
-    unsigned char* stage = ring + st * stage_bytes(HD);
-    if (nkeys - key0 < 16) {  // rows that no key fills weigh nothing, but must not hold NaN
-      for (int i = (nkeys - key0) * (HD / 8) + lane; i < 16 * (HD / 8); i += 32)
-        reinterpret_cast<uint4*>(stage + 16 * HD * 2)[i] = make_uint4(0, 0, 0, 0);
+  __device__ __forceinline__ void start(const Params& p, int b, int h0, int nh) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+      const long long at = ((long long)b * p.hq + h0 + min(g, nh - 1)) * HD + 32 * i + 8 * t;
+      if (TERMS > 1) {
+        const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at);
+        const float4 c = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at + 4);
+        float x[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int e = 0; e < TERMS; ++e)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            qb[e][i][s][0] = take_pair(x[4 * s], x[4 * s + 1]);
+            qb[e][i][s][1] = take_pair(x[4 * s + 2], x[4 * s + 3]);
+          }
+      } else {
+        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at);
+        qb[0][i][0][0] = a.x; qb[0][i][0][1] = a.y; qb[0][i][1][0] = a.z; qb[0][i][1][1] = a.w;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < HD / 16; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+  }
+
+  // The first n of the 16 keys in the stage (K [16][HD], V [16][HD]).
+  __device__ __forceinline__ void step(unsigned char* stage, int n, float scale_log2) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    if (n < 16) {  // rows that no key fills weigh nothing, but must not hold NaN
+      for (int i = n * (HD / 8) + lane; i < 16 * (HD / 8); i += 32) reinterpret_cast<uint4*>(stage + 16 * HD * 2)[i] = make_uint4(0, 0, 0, 0);
       __syncwarp();
     }
     uint4 kr[2][KI], vr[4][HD / 64];  // keys g, g + 8; keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
@@ -631,13 +590,13 @@ __global__ void __launch_bounds__(kThreads, TERMS == 1 ? 3 : 2) rows_kernel(cons
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int i = 0; i < KI; ++i) kr[j][i] = *reinterpret_cast<const uint4*>(stage + (g + 8 * j) * HD * 2 + 16 * t + 64 * i);
-    // the hardware's sums drop bits: the small terms first, in chains of their own
-    float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+    // the hardware's sums drop bits: the small terms in chains of their own
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[TERMS > 1 ? TERMS - 1 : 1][4] = {};
 #pragma unroll
     for (int e = TERMS - 1; e >= 0; --e)
 #pragma unroll
       for (int i = 0; i < KI; ++i) {
-        float* c = e > 0 ? s2 : s;
+        float* c = e > 0 ? s2[e - 1] : s;
         mma16816(c, kr[0][i].x, kr[1][i].x, kr[0][i].y, kr[1][i].y, qb[e][i][0][0], qb[e][i][0][1]);
         mma16816(c, kr[0][i].z, kr[1][i].z, kr[0][i].w, kr[1][i].w, qb[e][i][1][0], qb[e][i][1][1]);
       }
@@ -649,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, TERMS == 1 ? 3 : 2) rows_kernel(cons
     // s: (key g, heads 2t, 2t+1), (key g + 8, heads 2t, 2t+1)
     float al[2], pr[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] = key0 + g + 8 * (j >> 1) < nkeys ? (s[j] + s2[j]) * p.scale_log2 : -INFINITY;
+    for (int j = 0; j < 4; ++j) s[j] = g + 8 * (j >> 1) < n ? (TERMS > 1 ? s[j] + (s2[0][j] + s2[TERMS - 2 > 0 ? 1 : 0][j]) : s[j]) * scale_log2 : -INFINITY;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       float mx = fmaxf(s[j], s[j + 2]);
@@ -672,11 +631,9 @@ __global__ void __launch_bounds__(kThreads, TERMS == 1 ? 3 : 2) rows_kernel(cons
     uint32_t pb[TERMS][2];
 #pragma unroll
     for (int e = 0; e < TERMS; ++e) {
-      pb[e][0] = movm(take_pair(pr[0], pr[1]));
-      pb[e][1] = movm(take_pair(pr[2], pr[3]));
+      pb[e][0] = movm(take_prob(pr[0], pr[1]));
+      pb[e][1] = movm(take_prob(pr[2], pr[3]));
     }
-    // element e of this lane's two pieces of 8: rows g -> g * 8 + e and g + 8 -> 64 + g * 8 + e (hd 128), or
-    // g * 8 + 2 e and g * 8 + 2 e + 1 (hd 64)
     auto word = [&](int k, int i) {
       const uint4& x = vr[k][i >> 2];
       return (i & 3) == 0 ? x.x : (i & 3) == 1 ? x.y : (i & 3) == 2 ? x.z : x.w;
@@ -698,8 +655,129 @@ __global__ void __launch_bounds__(kThreads, TERMS == 1 ? 3 : 2) rows_kernel(cons
         for (int x = 0; x < 4; ++x) o[e][x] += c[x];
       }
     }
+  }
+  __device__ __forceinline__ void join_sums() {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      l[j] += __shfl_xor_sync(0xffffffffu, l[j], 4);
+      l[j] += __shfl_xor_sync(0xffffffffu, l[j], 8);
+      l[j] += __shfl_xor_sync(0xffffffffu, l[j], 16);
+    }
+  }
+  // o[e][x] belongs to head 2 t + (x & 1) and this element: rows g of the product are the low ones, rows g + 8 the high ones
+  static __device__ __forceinline__ int element(int e, int x, int g) {
+    return HD == 128 ? (x < 2 ? 0 : 64) + g * 8 + e : g * 8 + 2 * e + (x < 2 ? 0 : 1);
+  }
+};
+
+// The rows [k0, k0 + n) of keys of which the first P lie in the prefix, into a stage.
+template <int HD>
+__device__ __forceinline__ void fetch(const Params& p, unsigned char* dst, uint64_t* bar, int b, int kh, int P, int k0, int n, uint64_t pol) {
+  const int a = max(0, min(n, P - k0));
+  mbar_arrive_expect_tx(bar, (uint32_t)n * HD * 4);
+  if (a > 0) {
+    const long long at = ((long long)kh * p.prefix_cap + k0) * HD;
+    bulk_g2s(dst, p.pk + at, a * HD * 2, bar, pol);
+    bulk_g2s(dst + 16 * HD * 2, p.pv + at, a * HD * 2, bar, pol);
+  }
+  if (a < n) {
+    const long long at = (((long long)b * p.hkv + kh) * p.max_seq + (k0 + a - P)) * HD;
+    bulk_g2s(dst + a * HD * 2, p.kc + at, (n - a) * HD * 2, bar, pol);
+    bulk_g2s(dst + (16 + a) * HD * 2, p.vc + at, (n - a) * HD * 2, bar, pol);
+  }
+}
+
+// Four outputs; a sequence without keys gives 0, a bad length or a given-up wait NaN.
+template <int TERMS>
+__device__ __forceinline__ void store4(const Params& p, long long at, float4 y, float sum, bool nan, bool none) {
+  const float inv = 1.0f / sum;
+  y.x *= inv; y.y *= inv; y.z *= inv; y.w *= inv;
+  if (nan) y = make_float4(NAN, NAN, NAN, NAN);
+  else if (none) y = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (TERMS > 1) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = y;
+  } else {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
+}
+__device__ __forceinline__ void add4(float4& y, float w, const float4& v) {
+  y.x = fmaf(w, v.x, y.x); y.y = fmaf(w, v.y, y.y); y.z = fmaf(w, v.z, y.z); y.w = fmaf(w, v.w, y.w);
+}
+
+// ---------------------------------------------------------------------------------------------
+// rows kernel: all keys of a sequence, where the prefix is short
+// ---------------------------------------------------------------------------------------------
+// The sum over a cluster's blocks goes through their shared memory.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t remote_addr(const void* p, int rank) {  // the same place in another block of the cluster
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float remote(const float* p, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 remote4(const float* p, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(remote_addr(p, rank)) : "memory");
+  return v;
+}
+
+// Shared memory: the warps' rings (afterwards O, maxima and sums of the warps, and of the block), the barriers.
+__host__ __device__ constexpr int rows_smem(int warps, int hd) { return warps * kRing * (stage_bytes(hd) + 8); }
+
+// A block of W warps, or a cluster of CS blocks, per (sequence, kv head, 8 query heads); steps are dealt in turn.
+template <int HD, int TERMS>
+__global__ void __launch_bounds__(kThreads, TERMS == 1 ? 3 : 2) rows_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int W = blockDim.x >> 5;
+  float* s_o = reinterpret_cast<float*>(smem);  // [warp][head][HD], over the rings
+  float* s_m = s_o + W * kHeads * HD;           // [warp][head]
+  float* s_l = s_m + W * kHeads;                // [warp][head]
+  static_assert(kRing * stage_bytes(HD) >= kHeads * (HD + 2) * 4, "a warp's sums fit over its ring");
+  __shared__ int s_fail;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int CS = p.row_cluster, rank = blockIdx.x % CS, pair = blockIdx.x / CS;
+  const int hb = pair % p.hblocks, kh = pair / p.hblocks % p.hkv, b = pair / p.hblocks / p.hkv;
+  const int h0 = kh * p.gq + hb * kHeads, nh = min(kHeads, p.gq - hb * kHeads);
+  unsigned char* ring = smem + warp * kRing * stage_bytes(HD);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + W * kRing * stage_bytes(HD)) + warp * kRing;
+  if (lane == 0) {
+    for (int i = 0; i < kRing; ++i) mbar_init(&bar[i], 1);
+    fence_mbar_init();
+  }
+  if (tid == 0) s_fail = 0;
+  pdl_wait();
+  pdl_trigger();
+  const int len = p.max_seq > 0 ? p.lens[b] : 0;
+  const bool bad = len < 0 || len > p.max_seq;
+  const int nkeys = bad ? 0 : p.P + len, key_step = CS * W * 16;
+  int key0 = (rank * W + warp) * 16;
+  const uint64_t pol = l2_evict_first_policy();
+  if (lane == 0)
+    for (int i = 0; i < kRing; ++i) {
+      const int k = key0 + i * key_step;
+      if (k < nkeys) fetch<HD>(p, ring + i * stage_bytes(HD), &bar[i], b, kh, p.P, k, min(16, nkeys - k), pol);
+    }
+  Rows<HD, TERMS> r;
+  r.start(p, b, h0, nh);
+  __syncwarp();  // the barriers are set up
+  bool ok = true;
+  int st = 0;
+  uint32_t ph = 0;
+  for (; key0 < nkeys; key0 += key_step) {
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[st], ph)) != 0;
+    r.step(ring + st * stage_bytes(HD), min(16, nkeys - key0), p.scale_log2);
     __syncwarp();  // every lane has read the stage
-    if (lane == 0 && ok && key0 + kRing * key_step < nkeys) fetch(st, key0 + kRing * key_step);
+    const int k = key0 + kRing * key_step;
+    if (lane == 0 && ok && k < nkeys) fetch<HD>(p, ring + st * stage_bytes(HD), &bar[st], b, kh, p.P, k, min(16, nkeys - k), pol);
     if (++st == kRing) { st = 0; ph ^= 1; }
   }
   if (!ok) {  // a wait gave up: the copies in flight land, the row comes out NaN
@@ -707,39 +785,26 @@ __global__ void __launch_bounds__(kThreads, TERMS == 1 ? 3 : 2) rows_kernel(cons
     s_fail = 1;
   }
   __syncthreads();  // the rings are read, and the sums may lie over them
-  // this warp's part
+  r.join_sums();
+  if (g == 0)
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 4);
-    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 8);
-    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 16);
-    if (g == 0) {
-      s_m[warp * kHeads + 2 * t + j] = m[j];
-      s_l[warp * kHeads + 2 * t + j] = l[j];
+    for (int j = 0; j < 2; ++j) {
+      s_m[warp * kHeads + 2 * t + j] = r.m[j];
+      s_l[warp * kHeads + 2 * t + j] = r.l[j];
     }
-  }
 #pragma unroll
-  for (int e = 0; e < HD / 16; ++e) {
-    const int lo = HD == 128 ? g * 8 + e : g * 8 + 2 * e, hi = HD == 128 ? 64 + g * 8 + e : g * 8 + 2 * e + 1;
-    float* d0 = s_o + (warp * kHeads + 2 * t) * HD;
-    d0[lo] = o[e][0]; d0[HD + lo] = o[e][1]; d0[hi] = o[e][2]; d0[HD + hi] = o[e][3];
-  }
+  for (int e = 0; e < HD / 16; ++e)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) s_o[(warp * kHeads + 2 * t + (x & 1)) * HD + r.element(e, x, g)] = r.o[e][x];
   __syncthreads();
-  // The parts of a row: W warps of this block, or the blocks of the cluster (each first adds up its own warps, in the place
-  // of its first), then the prefix kernel's.
-  auto combine = [&](float& y, float w, float v) { y = fmaf(w, v, y); };
-  if (CS > 1) {
+  if (CS > 1) {  // the block's own sum first, in the place of its first warp's
     for (int i = tid; i < nh * (HD / 4); i += blockDim.x) {
       const int h = i / (HD / 4), d = i % (HD / 4) * 4;
       float mx = -INFINITY;
       for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[w * kHeads + h]);
       const float mu = mx == -INFINITY ? 0.f : mx;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < W; ++w) {
-        const float a = ex2(s_m[w * kHeads + h] - mu);
-        const float4 v = *reinterpret_cast<const float4*>(s_o + (w * kHeads + h) * HD + d);
-        combine(y.x, a, v.x); combine(y.y, a, v.y); combine(y.z, a, v.z); combine(y.w, a, v.w);
-      }
+      for (int w = 0; w < W; ++w) add4(y, ex2(s_m[w * kHeads + h] - mu), *reinterpret_cast<const float4*>(s_o + (w * kHeads + h) * HD + d));
       *reinterpret_cast<float4*>(s_o + h * HD + d) = y;  // read by this thread only
     }
     __syncthreads();
@@ -749,137 +814,220 @@ __global__ void __launch_bounds__(kThreads, TERMS == 1 ? 3 : 2) rows_kernel(cons
       const float mu = mx == -INFINITY ? 0.f : mx;
       for (int w = 0; w < W; ++w) lt += s_l[w * kHeads + tid] * ex2(s_m[w * kHeads + tid] - mu);
       s_m[tid] = mx;
-      s_l[tid] = lt;
+      s_l[tid] = s_fail ? NAN : lt;
     }
     cluster_sync();
   }
-  pdl_wait();  // the prefix kernel's parts are there (every block waits, so that this grid ends after that one)
-  const int nw = CS > 1 ? CS : W;
-  const bool none = p.P == 0 && len == 0;
   if (rank == 0) {
-    // the row's parts of the prefix: slots first + u .. last + u of its unit
-    __shared__ long long s_at[kHeads];
-    __shared__ int s_np[kHeads];
-    auto prefix_parts = [&](int h, int* np) {
-      const int prow = b * p.gq + hb * kHeads + h, u = kh * p.units_per_kv + prow / (NS * kTile);
-      if (!p.use_prefix) {
-        *np = 0;
-        return 0LL;
-      }
-      const long long total = (long long)p.units * p.nch;
-      int first;
-      if (total * p.n_cta < 0x7fffffffLL) {  // 32-bit divisions where they do
-        first = ((u * p.nch + 1) * p.n_cta - 1) / (int)total;
-        *np = ((u + 1) * p.nch * p.n_cta - 1) / (int)total - first + 1;
-      } else {
-        first = (int)((((long long)u * p.nch + 1) * p.n_cta - 1) / total);
-        *np = (int)(((long long)(u + 1) * p.nch * p.n_cta - 1) / total) - first + 1;
-      }
-      return (long long)(first + u) * (NS * kTile) + prow % (NS * kTile);
-    };
-    // Weights of the parts: 4 W neighbouring lanes a head, all heads at once.
-    {
-      const int L = 4 * W, h = min(tid / L, nh - 1), l0 = tid % L;  // heads that do not exist repeat the last one
-      int np;
-      const long long at = prefix_parts(h, &np);
-      const float2* ml = p.part_ml + at;
-      float* wt = s_w + h * p.parts;
-      const int n = nw + np;
-      auto get = [&](int j) {
-        return j < nw ? (CS > 1 ? make_float2(remote(&s_m[h], j), remote(&s_l[h], j)) : make_float2(s_m[j * kHeads + h], s_l[j * kHeads + h]))
-                      : __ldcg(ml + (long long)(j - nw) * NS * kTile);
-      };
-      float mx = -INFINITY, lt = 0.f;
-      for (int j = l0; j < n; j += 4 * L) {
-        float2 v[4];
+    const int nw = CS > 1 ? CS : W;  // at most 8
+    for (int i = tid; i < nh * (HD / 4); i += blockDim.x) {
+      const int h = i / (HD / 4), d = i % (HD / 4) * 4;
+      float mw[8], lw[8], mx = -INFINITY, lt = 0.f;
+      float4 v[8], y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) v[x] = j + x * L < n ? get(j + x * L) : make_float2(-INFINITY, 0.f);
-        const float mn = fmaxf(fmaxf(mx, fmaxf(v[0].x, v[1].x)), fmaxf(v[2].x, v[3].x)), mu = mn == -INFINITY ? 0.f : mn;
-        lt *= ex2(mx - mu);
+      for (int j = 0; j < 8; ++j)
+        if (j < nw) {
+          mw[j] = CS > 1 ? remote(&s_m[h], j) : s_m[j * kHeads + h];
+          lw[j] = CS > 1 ? remote(&s_l[h], j) : s_l[j * kHeads + h];
+          v[j] = CS > 1 ? remote4(s_o + h * HD + d, j) : *reinterpret_cast<const float4*>(s_o + (j * kHeads + h) * HD + d);
+          mx = fmaxf(mx, mw[j]);
+        }
+      const float mu = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          lt += v[x].y * ex2(v[x].x - mu);
-          if (j + x * L < n && tid / L < nh) wt[j + x * L] = v[x].x;
+      for (int j = 0; j < 8; ++j)
+        if (j < nw) {
+          const float w = ex2(mw[j] - mu);
+          lt = fmaf(w, lw[j], lt);
+          add4(y, w, v[j]);
         }
-        mx = mn;
-      }
-      float ma = mx;
-      for (int x = L >> 1; x; x >>= 1) ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, x));
-      const float mu = ma == -INFINITY ? 0.f : ma;
-      lt *= ex2(mx - mu);
-      for (int x = L >> 1; x; x >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, x);
-      if (tid / L < nh) {
-        for (int j = l0; j < n; j += L) wt[j] = ex2(wt[j] - mu);
-        if (l0 == 0) {
-          s_at[h] = at;
-          s_np[h] = np;
-          s_sum[h] = lt;
-          if (p.lse) p.lse[(long long)b * p.hq + h0 + h] = bad || s_fail ? NAN : none ? -INFINITY : ma * kLn2 + logf(lt);
-        }
-      }
+      const bool nan = bad || s_fail, none = nkeys == 0;
+      store4<TERMS>(p, ((long long)b * p.hq + h0 + h) * HD + d, y, lt, nan, none);
+      if (d == 0 && p.lse) p.lse[(long long)b * p.hq + h0 + h] = nan ? NAN : none ? -INFINITY : mx * kLn2 + logf(lt);
     }
-    __syncthreads();
-    // Four elements of a head a thread and item; neighbours take the heads, whose rows lie side by side in a part.  A few
-    // items' loads, or a few parts', are under way together.
-    const int items = nh * (HD / 4);
-    auto outputs = [&](auto n_items, auto n_parts) {
-      constexpr int NI = decltype(n_items)::value, NP = decltype(n_parts)::value;
-      for (int i0 = tid; i0 < items; i0 += NI * blockDim.x) {
-        float4 y[NI];
-        const float* src[NI];
-        const float* wt[NI];
-        int most = 0, np[NI];
-#pragma unroll
-        for (int x = 0; x < NI; ++x) {
-          const int i = min(i0 + x * (int)blockDim.x, items - 1), h = i % nh, d = i / nh * 4;
-          y[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-          np[x] = s_np[h];
-          most = max(most, np[x]);
-          wt[x] = s_w + h * p.parts;
-          src[x] = p.part + s_at[h] / kTile * (kTile * HD) + d * kTile + s_at[h] % kTile * 4;
-        }
-        auto add = [&](float4& y, float w, const float4& v) {
-          combine(y.x, w, v.x); combine(y.y, w, v.y); combine(y.z, w, v.z); combine(y.w, w, v.w);
-        };
-        for (int j = 0; j < most; j += NP) {
-          float4 v[NP][NI];
-#pragma unroll
-          for (int k = 0; k < NP; ++k)
-#pragma unroll
-            for (int x = 0; x < NI; ++x)
-              if (j + k < np[x]) v[k][x] = __ldcg(reinterpret_cast<const float4*>(src[x] + (long long)(j + k) * NS * kTile * HD));
-#pragma unroll
-          for (int k = 0; k < NP; ++k)
-#pragma unroll
-            for (int x = 0; x < NI; ++x)
-              if (j + k < np[x]) add(y[x], wt[x][nw + j + k], v[k][x]);
-        }
-#pragma unroll
-        for (int x = 0; x < NI; ++x) {
-          const int i = i0 + x * (int)blockDim.x;
-          if (i >= items) break;
-          const int h = i % nh, d = i / nh * 4;
-          for (int j = 0; j < nw; ++j)
-            add(y[x], wt[x][j], CS > 1 ? remote4(s_o + h * HD + d, j) : *reinterpret_cast<const float4*>(s_o + (j * kHeads + h) * HD + d));
-          const float inv = 1.0f / s_sum[h];
-          float4 o4 = make_float4(y[x].x * inv, y[x].y * inv, y[x].z * inv, y[x].w * inv);
-          if (bad || s_fail) o4 = make_float4(NAN, NAN, NAN, NAN);
-          else if (none) o4 = make_float4(0.f, 0.f, 0.f, 0.f);
-          const long long at = ((long long)b * p.hq + h0 + h) * HD + d;
-          if (TERMS > 1) {
-            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = o4;
-          } else {
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(o4.x, o4.y), hi = __floats2bfloat162_rn(o4.z, o4.w);
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-          }
-        }
-      }
-    };
-    if (items > 2 * (int)blockDim.x) outputs(Int<4>(), Int<4>());
-    else outputs(Int<1>(), Int<12>());
   }
   if (CS > 1) cluster_sync();  // nobody reads this block's shared memory any more
+}
+
+// ---------------------------------------------------------------------------------------------
+// parts kernel: the sequences' own keys, beside the prefix kernel
+// ---------------------------------------------------------------------------------------------
+// A block is one warp with a run of `own_run` keys of a (sequence, kv head, 8 query heads): small enough that two of them
+// find room on an SM beside a block of the prefix kernel, and nine when that is done.  Its part: O [8 heads][hd] and (maximum,
+// sum) of the 8 heads.  The first runs of all pairs come first, the longest by their lengths.
+template <int HD, int TERMS>
+__global__ void __launch_bounds__(32, 12) parts_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ __align__(8) uint64_t bar[kRing];
+  const int lane = threadIdx.x, g = lane >> 2, t = lane & 3;
+  const int pairs = p.B * p.hkv * p.hblocks, run = blockIdx.x / pairs, pair = blockIdx.x - run * pairs;
+  const int hb = pair % p.hblocks, kh = pair / p.hblocks % p.hkv, b = pair / p.hblocks / p.hkv;
+  const int len = __ldg(p.lens + b), k0 = run * p.own_run, k1 = len > p.max_seq ? 0 : min(len, k0 + p.own_run);
+  pdl_trigger();  // the join kernel may come in when the last of these blocks has started
+  if (k0 < k1) {  // else no part: the length says so
+    if (lane == 0) {
+      for (int i = 0; i < kRing; ++i) mbar_init(&bar[i], 1);
+      fence_mbar_init();
+    }
+    __syncwarp();
+    const uint64_t pol = l2_evict_first_policy();
+    const long long at = (((long long)b * p.hkv + kh) * p.max_seq + k0) * HD;
+    const __nv_bfloat16 *ks = p.kc + at, *vs = p.vc + at;
+    auto issue = [&](int st, int k) {  // keys k .. of the run
+      const uint32_t bytes = min(16, k1 - k0 - k) * HD * 2;
+      mbar_arrive_expect_tx(&bar[st], 2 * bytes);
+      bulk_g2s(ring + st * stage_bytes(HD), ks + (long long)k * HD, bytes, &bar[st], pol);
+      bulk_g2s(ring + st * stage_bytes(HD) + 16 * HD * 2, vs + (long long)k * HD, bytes, &bar[st], pol);
+    };
+    if (lane == 0)
+      for (int i = 0; i < kRing; ++i)
+        if (16 * i < k1 - k0) issue(i, 16 * i);
+    Rows<HD, TERMS> r;
+    r.start(p, b, kh * p.gq + hb * kHeads, min(kHeads, p.gq - hb * kHeads));
+    bool ok = true;
+    int st = 0;
+    uint32_t ph = 0;
+    for (int k = 0; k < k1 - k0; k += 16) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[st], ph)) != 0;
+      r.step(ring + st * stage_bytes(HD), min(16, k1 - k0 - k), p.scale_log2);
+      __syncwarp();  // every lane has read the stage
+      if (lane == 0 && ok && k + 16 * kRing < k1 - k0) issue(st, k + 16 * kRing);
+      if (++st == kRing) { st = 0; ph ^= 1; }
+    }
+    r.join_sums();
+    const size_t part = (size_t)pair * p.own_runs + run;
+    __syncwarp();  // the ring is read: O goes through it, to be written in rows
+    float* so = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int e = 0; e < HD / 16; ++e)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) so[(2 * t + (x & 1)) * (HD + 4) + r.element(e, x, g)] = r.o[e][x];
+    __syncwarp();
+    float4* po = p.own + part * (kHeads * HD / 4);
+#pragma unroll
+    for (int i = lane; i < kHeads * HD / 4; i += 32) po[i] = *reinterpret_cast<const float4*>(so + i / (HD / 4) * (HD + 4) + i % (HD / 4) * 4);
+    if (g == 0)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) p.own_ml[part * kHeads + 2 * t + j] = make_float2(r.m[j], ok ? r.l[j] : NAN);  // NaN: a wait gave up
+    if (!ok)  // the copies in flight land before the block leaves
+      for (int i = 0; i < kRing; ++i) mbar_wait_bounded(&bar[(st + i) % kRing], ph ^ (st + i >= kRing), 10000000ull);
+  }
+  // One block ends only after the prefix kernel, so that the end of this kernel is the end of both; the others make room.
+  if (blockIdx.x == gridDim.x - 1) pdl_wait();
+}
+
+// ---------------------------------------------------------------------------------------------
+// join kernel: the parts of a row
+// ---------------------------------------------------------------------------------------------
+constexpr int kJoin = 128;  // threads: 16 a head for the weights, then four elements of a head each
+
+template <int HD, int TERMS>
+__global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Params p) {
+  constexpr int NS = Cfg<HD, TERMS>::kSlots, L = kJoin / kHeads;
+  constexpr int kEarly = 8;  // parts of a thread's first output that are on their way while the weights are formed
+  extern __shared__ __align__(16) float s_w[];  // [head][part]: the weights
+  __shared__ float s_sum[kHeads];
+  const int tid = threadIdx.x, pair = blockIdx.x;
+  const int hb = pair % p.hblocks, kh = pair / p.hblocks % p.hkv, b = pair / p.hblocks / p.hkv;
+  const int h0 = kh * p.gq + hb * kHeads, nh = min(kHeads, p.gq - hb * kHeads);
+  // a row's parts of the prefix: slots first + u .. last + u of its unit; the first one's row, and how many
+  auto prefix_parts = [&](int h, int* np) {
+    const int row = b * p.gq + hb * kHeads + h, u = kh * p.units_per_kv + row / (NS * kTile);
+    const long long total = (long long)p.units * p.nch;
+    int first;
+    if (total * p.n_cta < 0x7fffffffLL) {  // 32-bit divisions where they do
+      first = ((u * p.nch + 1) * p.n_cta - 1) / (int)total;
+      *np = ((u + 1) * p.nch * p.n_cta - 1) / (int)total - first + 1;
+    } else {
+      first = (int)((((long long)u * p.nch + 1) * p.n_cta - 1) / total);
+      *np = (int)(((long long)(u + 1) * p.nch * p.n_cta - 1) / total) - first + 1;
+    }
+    return (long long)(first + u) * (NS * kTile) + row % (NS * kTile);
+  };
+  const int hw = min(tid / L, nh - 1), l0 = tid % L;  // weights: 16 lanes a head; heads that do not exist repeat the last one
+  int np_w, np = 0;
+  const float2* ml = p.part_ml + prefix_parts(hw, &np_w);
+  pdl_wait();
+  pdl_trigger();
+  const int len = p.max_seq > 0 ? __ldg(p.lens + b) : 0;
+  const bool bad = len < 0 || len > p.max_seq;
+  const int no = bad || len == 0 ? 0 : (len + p.own_run - 1) / p.own_run;
+  // Outputs: four elements of a head a thread; neighbours take the heads, whose rows lie side by side in a prefix part.
+  const float4 *own = nullptr, *pre = nullptr;
+  auto aim = [&](int i) {
+    const int h = i % nh, d4 = i / nh;
+    const long long at = prefix_parts(h, &np);
+    own = p.own + (size_t)pair * p.own_runs * (kHeads * HD / 4) + h * (HD / 4) + d4;
+    pre = reinterpret_cast<const float4*>(p.part) + at / kTile * (kTile * HD / 4) + d4 * kTile + at % kTile;
+  };
+  auto part = [&](int j) { return __ldcg(j < no ? own + (size_t)j * (kHeads * HD / 4) : pre + (long long)(j - no) * (NS * kTile * HD / 4)); };
+  const int items = nh * (HD / 4);
+  float4 early[kEarly];
+  if (tid < items) {
+    aim(tid);
+#pragma unroll
+    for (int x = 0; x < kEarly; ++x)
+      if (x < no + np) early[x] = part(x);
+  }
+  {
+    const float2* oml = p.own_ml + (size_t)pair * p.own_runs * kHeads + hw;
+    float* wt = s_w + hw * p.parts;
+    const int n = no + np_w;
+    float mx = -INFINITY, lt = 0.f;
+    for (int j = l0; j < n; j += 4 * L) {
+      float2 v[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int i = j + x * L;
+        v[x] = i < no ? __ldcg(oml + i * kHeads) : i < n ? __ldcg(ml + (long long)(i - no) * NS * kTile) : make_float2(-INFINITY, 0.f);
+      }
+      const float mn = fmaxf(fmaxf(mx, fmaxf(v[0].x, v[1].x)), fmaxf(v[2].x, v[3].x)), mu = mn == -INFINITY ? 0.f : mn;
+      lt *= ex2(mx - mu);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        lt += v[x].y * ex2(v[x].x - mu);
+        if (j + x * L < n && tid / L < nh) wt[j + x * L] = v[x].x;
+      }
+      mx = mn;
+    }
+    float ma = mx;
+#pragma unroll
+    for (int x = L >> 1; x; x >>= 1) ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, x));
+    const float mu = ma == -INFINITY ? 0.f : ma;
+    lt *= ex2(mx - mu);
+#pragma unroll
+    for (int x = L >> 1; x; x >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, x);
+    if (tid / L < nh) {
+      for (int j = l0; j < n; j += L) wt[j] = ex2(wt[j] - mu);
+      if (l0 == 0) {
+        s_sum[hw] = lt;
+        if (p.lse) p.lse[(long long)b * p.hq + h0 + hw] = bad ? NAN : ma * kLn2 + logf(lt);
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < items; i += kJoin) {
+    if (i != tid) aim(i);
+    const int h = i % nh, n = no + np;
+    const float* wt = s_w + h * p.parts;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    int j = 0;
+    if (i == tid) {
+#pragma unroll
+      for (int x = 0; x < kEarly; ++x)
+        if (x < n) add4(y, wt[x], early[x]);
+      j = kEarly;
+    }
+    for (; j < n; j += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (j + x < n) v[x] = part(j + x);
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (j + x < n) add4(y, wt[j + x], v[x]);
+    }
+    store4<TERMS>(p, ((long long)b * p.hq + h0 + h) * HD + i / nh * 4, y, s_sum[h], bad, false);
+  }
 }
 
 // Prefix keys through the tensor cores, or read by the rows kernel of every sequence: the tensor cores' part costs some 8 us
@@ -892,11 +1040,14 @@ bool prefix_pays(int B, int hkv, int hd, int P) { return (long long)B * hkv * P 
 void prefix_geometry(int rows, int hkv, int P, int ns, int sms, Params* p) {
   p->units_per_kv = (rows + ns * kTile - 1) / (ns * kTile);
   p->units = hkv * p->units_per_kv;
+  p->tiles = rows <= kTile ? 1 : ns;  // tiles that a unit can have
   p->nch = (P + kTile - 1) / kTile;
   const long long total = (long long)p->units * p->nch;
   p->n_cta = (int)(total < sms ? total : sms);
 }
 size_t part_rows(const Params& p, int ns) { return ((size_t)p.n_cta + p.units) * ns * kTile; }
+// Runs of a sequence's own keys: 4096 parts in all where the batch is smaller, 16 of a sequence at most.
+int most_own_runs(long long pairs) { return pairs >= 4096 ? 1 : 4096 / pairs < 16 ? (int)(4096 / pairs) : 16; }
 
 cudaError_t encode_map(CUtensorMap* out, const void* base, int hd, int P, int cap, int hkv) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
@@ -934,64 +1085,76 @@ cudaError_t launch(Params& p, void* workspace, cudaStream_t s) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 64 || !set[dev]) {
-      e = cudaFuncSetAttribute(prefix_kernel<HD, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+      e = cudaFuncSetAttribute(prefix_kernel<HD, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(C::kSlots));
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(rows_kernel<HD, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 rows_smem(kWarps, HD, 8 + num_sms()));
+                                 rows_smem(kWarps, HD));
+      // all of the SM's memory as shared memory, so that blocks of both kernels fit beside one another
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(prefix_kernel<HD, TERMS>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(parts_kernel<HD, TERMS>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
       if (e != cudaSuccess) return e;
       if (dev < 64) set[dev] = true;
     }
   }
-  if (p.use_prefix) {
-    prefix_geometry(p.B * p.gq, p.hkv, p.P, C::kSlots, num_sms(), &p);
-    p.part = static_cast<float*>(workspace);
-    p.part_ml = reinterpret_cast<float2*>(p.part + part_rows(p, C::kSlots) * HD);
-    PrefixMaps maps;
-    e = encode_map(&maps.k, p.pk, HD, p.P, (int)p.prefix_cap, p.hkv);
-    if (e == cudaSuccess) e = encode_map(&maps.v, p.pv, HD, p.P, (int)p.prefix_cap, p.hkv);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t pc;
-    memset(&pc, 0, sizeof(pc));
-    pc.gridDim = dim3((unsigned)p.n_cta);
-    pc.blockDim = dim3(C::kThreads);
-    pc.dynamicSmemBytes = C::kSmem;
-    pc.stream = s;
-    cudaLaunchAttribute pa[1];
-    pa[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pa[0].val.programmaticStreamSerializationAllowed = 1;
-    pc.attrs = pa;
-    pc.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&pc, prefix_kernel<HD, TERMS>, p, maps)) != cudaSuccess) return e;
-  }
-  // Warps of a pair (sequence, kv head): as many as run at once (8 an SM, by their rings), and enough for a warp to take 1024
-  // keys at most of a full cache; where 4 are too few, blocks in a cluster.
-  const long long pairs = (long long)p.B * p.hkv * p.hblocks, keys = p.max_seq + (p.use_prefix ? 0 : p.P);
-  int warps = 1;
-  while (warps < kWarps * 8 && warps * 16 < keys && (pairs * warps * 2 <= 8LL * num_sms() || warps * 1024 < keys)) warps *= 2;
-  p.row_cluster = warps > kWarps ? warps / kWarps : 1;
-  warps /= p.row_cluster;
-  p.parts = 8 + (p.use_prefix ? p.n_cta : 0);  // warps or blocks of a cluster: 8 at most
+  const int sms = num_sms();
+  const long long pairs = (long long)p.B * p.hkv * p.hblocks;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)(pairs * p.row_cluster));
-  cfg.blockDim = dim3((unsigned)(32 * warps));
-  cfg.dynamicSmemBytes = (size_t)rows_smem(warps, HD, p.parts);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  int n = 0;
-  if (p.use_prefix) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (p.row_cluster > 1) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = (unsigned)p.row_cluster;
-    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-    ++n;
-  }
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, rows_kernel<HD, TERMS>, p);
+  cfg.numAttrs = 1;
+  if (!p.use_prefix) {
+    // Warps of a pair (sequence, kv head): as many as run at once (8 an SM, by their rings), and enough for a warp to take
+    // 1024 keys at most of a full cache; where 4 are too few, blocks in a cluster.
+    const long long keys = p.max_seq + p.P;
+    int warps = 1;
+    while (warps < kWarps * 8 && warps * 16 < keys && (pairs * warps * 2 <= 8LL * sms || warps * 1024 < keys)) warps *= 2;
+    p.row_cluster = warps > kWarps ? warps / kWarps : 1;
+    warps /= p.row_cluster;
+    cfg.gridDim = dim3((unsigned)(pairs * p.row_cluster));
+    cfg.blockDim = dim3((unsigned)(32 * warps));
+    cfg.dynamicSmemBytes = (size_t)rows_smem(warps, HD);
+    if (p.row_cluster > 1) {
+      attr[1].id = cudaLaunchAttributeClusterDimension;
+      attr[1].val.clusterDim.x = (unsigned)p.row_cluster;
+      attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+      cfg.numAttrs = 2;
+    }
+    return cudaLaunchKernelEx(&cfg, rows_kernel<HD, TERMS>, p);
+  }
+  prefix_geometry(p.B * p.gq, p.hkv, p.P, C::kSlots, sms, &p);
+  const int most = most_own_runs(pairs);
+  p.part = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part + part_rows(p, C::kSlots) * HD);
+  p.own_ml = p.part_ml + part_rows(p, C::kSlots);
+  p.own = reinterpret_cast<float4*>(p.own_ml + (size_t)pairs * most * kHeads);
+  p.own_run = p.max_seq > 0 ? (int)((p.max_seq + most - 1) / most + 15) / 16 * 16 : 16;
+  if (p.own_run < 128) p.own_run = 128;
+  p.own_runs = p.max_seq > 0 ? (int)((p.max_seq + p.own_run - 1) / p.own_run) : 1;
+  p.parts = p.own_runs + p.n_cta;
+  PrefixMaps maps;
+  e = encode_map(&maps.k, p.pk, HD, p.P, (int)p.prefix_cap, p.hkv);
+  if (e == cudaSuccess) e = encode_map(&maps.v, p.pv, HD, p.P, (int)p.prefix_cap, p.hkv);
+  if (e != cudaSuccess) return e;
+  // Three kernels in one stream, each allowed to start beside the one before: the prefix kernel waits for what came before
+  // the call, and only then lets the parts kernel in beside it, which ends after it; the join kernel waits for that.
+  cfg.gridDim = dim3((unsigned)p.n_cta);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::smem(p.tiles);
+  if ((e = cudaLaunchKernelEx(&cfg, prefix_kernel<HD, TERMS>, p, maps)) != cudaSuccess) return e;
+  if (p.max_seq > 0) {
+    cfg.gridDim = dim3((unsigned)(pairs * p.own_runs));
+    cfg.blockDim = dim3(32);
+    cfg.dynamicSmemBytes = (size_t)kRing * stage_bytes(HD);
+    if ((e = cudaLaunchKernelEx(&cfg, parts_kernel<HD, TERMS>, p)) != cudaSuccess) return e;
+  }
+  cfg.gridDim = dim3((unsigned)pairs);
+  cfg.blockDim = dim3(kJoin);
+  cfg.dynamicSmemBytes = (size_t)kHeads * p.parts * 4;
+  return cudaLaunchKernelEx(&cfg, join_kernel<HD, TERMS>, p);
 }
 
 bool sizes_ok(int B, int hq, int hkv, int hd, int P) {
@@ -1014,7 +1177,9 @@ extern "C" size_t spd_shared_prefix_attention_workspace_bytes(int32_t B, int32_t
     const size_t n = spa::part_rows(p, ns);
     rows = n > rows ? n : rows;
   }
-  return rows * (head_dim * sizeof(float) + sizeof(float2));
+  const long long pairs = (long long)B * n_kv_heads * ((n_heads / n_kv_heads + spa::kHeads - 1) / spa::kHeads);
+  return rows * (head_dim * sizeof(float) + sizeof(float2)) +
+         (size_t)pairs * spa::most_own_runs(pairs) * spa::kHeads * (head_dim * sizeof(float) + sizeof(float2));
 }
 
 extern "C" int spd_shared_prefix_attention(const void* q, int32_t q_dtype, const void* prefix_k, const void* prefix_v,
