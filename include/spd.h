@@ -412,7 +412,8 @@ int spd_rope_append(const spd_rope* rope, const void* q, int64_t q_stride, void*
 
 /* 4-bit weights with group scales: W[r][c] = (code[r][c] - zero[r][c / group]) * scale[r][c / group].
  *   codes  uint8 [rows][cols/2], even column in the low nibble;
- *   scales [rows][cols/group] in scale_dtype;  zeros uint8 [rows][cols/group], or NULL: all 8.
+ *   scales [rows][cols/group] in scale_dtype;  zeros uint8 [rows][cols/group] of 0..240 (larger ones count
+ *   as 240), or NULL: all 8.
  * group 32, 64 or 128; cols a multiple of group, at most 32768; rows >= 1.
  *
  * spd_q4_quantize makes them from a matrix [rows][cols] in `dtype`, rounding to nearest (ties to
@@ -435,7 +436,8 @@ int spd_q4_pack(const uint8_t* codes, const void* scales, const uint8_t* zeros, 
  * x [M] rows of cols elements and y [M] rows of `rows` elements, both in x_dtype, row m starting at
  * m * stride.  All groups share cols, group, scale_dtype and has_zeros.  fp32 vectors are multiplied
  * exactly (three bf16 terms each), bf16 vectors as they are (normalised ones as two bf16 terms);
- * sums are fp32 in an order fixed by the sizes.  Groups must not write the same y.  SPD_EINVAL on bad
+ * sums are fp32 in an order fixed by the sizes.  Groups must not write the same y, nor
+ * over an x.  SPD_EINVAL on bad
  * sizes, NULL pointers, or unaligned ones (packed weights 16 bytes, x, y and nw their element). */
 typedef struct spd_q4_group {
   const void* w;     /* spd_q4_pack's output */

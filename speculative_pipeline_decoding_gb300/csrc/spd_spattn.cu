@@ -7,21 +7,30 @@
 // prefix kernel (tcgen05): the queries of one kv head, all sequences' together, are the 128 rows of an MMA tile:
 //   S = Q K_c^T  (M 128 x N 128 keys x K hd, fp32 in TMEM);  P = exp2(S - m) goes back to TMEM as bf16, over S, and is the A
 //   operand of  O += P V_c  (M 128 x N hd x K 128 keys).
-// One thread per row holds the row's 128 scores in registers, its running maximum and sum.  O is rescaled only when the
-// maximum has grown by more than 8 (a factor of 256, which bf16's and fp32's exponents take without loss), so nearly never
-// after the first chunk.  K and V chunks of 128 keys come by TMA through a ring of shared-memory stages; the tensor maps end
-// at the prefix's length, so that rows beyond it are zeros whatever the buffer holds.  bf16 queries: two tiles a block
-// alternate, one in the tensor core while the other's softmax runs.  fp32 queries: one tile, Q and P as three bf16 terms.
+// One thread per row keeps the row's running maximum and sum; it reads its 128 scores in two halves, the first half twice,
+// so that 128 registers do.  O is rescaled only when the maximum has grown by more than 8 (a factor of 256, which bf16's and
+// fp32's exponents take without loss), so nearly never after the first chunk.  K and V chunks of 128 keys come by TMA
+// through a ring of shared-memory stages; the tensor maps end at the prefix's length, so that rows beyond it are zeros
+// whatever the buffer holds.  bf16 queries: two tiles a block alternate, one in the tensor core while the other's softmax
+// runs.  fp32 queries: one tile, Q and P as three bf16 terms (x = t0 + t1 + t2 to 24 bits), small terms first.  bf16
+// queries' probabilities are rounded to bf16 once, which adds to the output what its own rounding does (2^-9 of the rms).
 // The work, (row tiles) x (chunks), is cut into equal runs, one per SM; a run that crosses from one tile to the next leaves
-// a part for each.  A chunk (64 KB at hd 128) feeds 2 x 4.2 MMAC a tile: the memory bounds up to about 256 rows a kv head,
-// the tensor cores and exponentials beyond.
+// a part for each.  A chunk (64 KB at hd 128) is 2 x 2.1 M MACs a tile, 1024 cycles of tensor core, and 2790 cycles of an
+// SM's share of the memory: that bounds up to about 256 rows a kv head, softmax and tensor core beyond (measured a chunk of
+// two tiles: 850 cycles of exponentials, 400 of maxima, 2 x 1024 of MMAs).  Alone, 64 x 4 rows a kv head x 32768 keys take
+// 30 us (134 MB: 4.5 TB/s, 1.1 PFLOP/s).
 //
-// rows kernel: joins those parts with the sequence's own keys.  One block per (sequence, kv head, up to 8 query heads of its group).  Its warps take 32 keys in turn and
-// work on mma.sync m16n8k16: S^T = K Q^T (16 keys x 8 heads), then O^T += V^T P^T (16 head elements x 8 heads).  K and V go
-// from global memory straight into operand registers: the order of the head elements in a dot product is free, so a lane
-// reads 16 consecutive bytes; V's pairs of keys are put together with byte permutes.  fp32 queries and their
-// probabilities enter as three bf16 terms (exact), bf16 queries' probabilities as one (rounded to bf16, 2^-9 relative,
-// like the output).  Statistics and sums are fp32.
+// parts kernel: the sequences' own keys, beside the prefix kernel (compute against memory: 64 KB of shared memory and 24 K
+// registers are left for it).  A warp takes up to 256 keys (long caches: more) of a (sequence, kv head, up to 8 query heads
+// of its group), 16 at a time, on mma.sync m16n8k16: S^T = K Q^T (16 keys x 8 heads), then O^T += V^T P^T (16 head elements
+// x 8 heads).  K and V come by bulk copies, three steps ahead; the order of the head elements in a dot product is free, so a
+// lane reads 16 consecutive bytes, and V's pairs of keys are put together with byte permutes.  Bound by memory.
+//
+// join kernel: the parts of a row, weighted and added.  256 sequences x 512 own keys at most over 8192 shared ones: 87 us in
+// all for 306 MB (45 us at the copy bandwidth); the parts kernel's shared-memory reads and the prefix kernel's operands
+// share the SMs, so that beside one another each is slower than alone (52 and 74 us against 30 and 52).
+//
+// rows kernel: all keys of a sequence in one kernel, where the prefix is too short for the tensor cores to gain anything.
 #include <cudaTypedefs.h>
 
 #include <cmath>
@@ -102,8 +111,7 @@ __device__ __forceinline__ uint32_t take_prob(float& a, float& b) {
 // prefix kernel
 // ---------------------------------------------------------------------------------------------
 constexpr int kTile = 128;   // rows of a tile, keys of a chunk
-// A block leaves registers (128 a thread) and shared memory for a few warps of the rows kernel beside it, which reads the
-// sequences' own keys meanwhile.
+// A block leaves registers (128 a thread) and shared memory for two warps of the parts kernel beside it.
 template <int HD, int TERMS> struct Cfg {
   static constexpr int kSlots = TERMS == 1 ? 2 : 1;              // row tiles of a block
   static constexpr int kTB = HD / 64 * kTile * 128;              // bytes of a 128-row operand
@@ -255,7 +263,6 @@ prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMa
     return x;
   };
 
-  if (warp >= NS * 4) {
   if (warp == kCopyWarp) {
     if ((tid & 31) == 0) {
       int st = 0;
@@ -370,7 +377,6 @@ prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMa
       mbar_wait_bounded(&drain, 0);
     }
     __syncwarp();
-  }
   } else {
     const int slot = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;

@@ -297,6 +297,21 @@ def test_q4_gemv_strides_shared_and_own_vectors(spd):
     assert torch.equal(y1, ys[0][1]) or (y1 - ys[0][1]).abs().max() <= 40 * U * float((x0[1].abs().double() @ raw[0].abs().T).max())
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_q4_gemv_zero_points_beyond_the_codes(spd, group):
+    """Zero points up to 240 are taken exactly, larger ones as 240."""
+    g = _g(16)
+    codes = torch.randint(0, 256, (50, 192 if group < 128 else 256), generator=g, device="cuda").to(torch.uint8)
+    cols = codes.size(1) * 2
+    scales = (0.5 + torch.rand(50, cols // group, generator=g, device="cuda")) * 0.01
+    zeros = torch.randint(0, 256, (50, cols // group), generator=g, device="cuda").to(torch.uint8)
+    x = _rn(g, 3, cols)
+    y = torch.empty(3, 50, device="cuda")
+    spd.q4_gemv([spd.q4_pack(codes, scales, zeros)], [x], [y])
+    W = _unpack(codes, scales, zeros.clamp(max=240))
+    _close(y, x.double() @ W.T, (cols / 16 + cols / group + 64) * U * (x.double().abs() @ W.abs().T))
+
+
 def test_q4_gemv_infinities_and_nan_stay_in_their_vector(spd):
     g = _g(10)
     c = spd.q4_quantize(_rn(g, 50, 256, std=0.02), 128)
