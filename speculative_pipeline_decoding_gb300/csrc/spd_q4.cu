@@ -564,6 +564,7 @@ int plan(Params* p, int sms) {
   p->mb = (p->M + parts - 1) / parts;
   int nt = (p->mb * p->terms + 7) / 8;
   if (nt > 4) nt = 6;
+  static_assert(96 * 1024 / (16 * (6 * 8 + 1) * 4) >= kWarps, "a batch holds a tile at least");
   const int own = (p->tiles + sms - 1) / sms, most = 96 * 1024 / (16 * (nt * 8 + 1) * 4) - kWarps + 1;
   p->batch = own < most ? own : most;
   for (int n = 1;; ++n) {

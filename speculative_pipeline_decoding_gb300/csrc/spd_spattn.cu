@@ -20,15 +20,14 @@
 // two tiles: 850 cycles of exponentials, 400 of maxima, 2 x 1024 of MMAs).  Alone, 64 x 4 rows a kv head x 32768 keys take
 // 30 us (134 MB: 4.5 TB/s, 1.1 PFLOP/s).
 //
-// parts kernel: the sequences' own keys, beside the prefix kernel (compute against memory: 64 KB of shared memory and 24 K
-// registers are left for it).  A warp takes up to 256 keys (long caches: more) of a (sequence, kv head, up to 8 query heads
-// of its group), 16 at a time, on mma.sync m16n8k16: S^T = K Q^T (16 keys x 8 heads), then O^T += V^T P^T (16 head elements
-// x 8 heads).  K and V come by bulk copies, three steps ahead; the order of the head elements in a dot product is free, so a
-// lane reads 16 consecutive bytes, and V's pairs of keys are put together with byte permutes.  Bound by memory.
+// parts kernel: the sequences' own keys, beside the prefix kernel (memory against compute: 60 KB of shared memory and 24 K
+// registers are left for it).  A warp takes 128 keys or more of a (sequence, kv head, up to 8 query heads of its group), 16
+// at a time, on mma.sync m16n8k16: S^T = K Q^T (16 keys x 8 heads), then O^T += V^T P^T (16 head elements x 8 heads).  K and
+// V come by tensor copies with the 128-byte swizzle, from which ldmatrix takes both operands without bank conflicts.
 //
-// join kernel: the parts of a row, weighted and added.  256 sequences x 512 own keys at most over 8192 shared ones: 87 us in
-// all for 306 MB (45 us at the copy bandwidth); the parts kernel's shared-memory reads and the prefix kernel's operands
-// share the SMs, so that beside one another each is slower than alone (52 and 74 us against 30 and 52).
+// join kernel: the parts of a row, weighted and added.  256 sequences of at most 512 own keys over 8192 shared ones: 85 us in
+// all for 306 MB (45 us at the copy bandwidth): beside one another the prefix kernel takes 57 us and the parts kernel 72
+// (alone 30 and 50), then the join 8.
 //
 // rows kernel: all keys of a sequence in one kernel, where the prefix is too short for the tensor cores to gain anything.
 #include <cudaTypedefs.h>
@@ -82,6 +81,12 @@ __device__ __forceinline__ uint32_t movm(uint32_t x) {  // transpose of an 8 x 8
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+__device__ __forceinline__ void ldsm(uint32_t* r, uint32_t a) {  // four 8 x 8 matrices of 16-bit elements, a row a lane
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t* r, uint32_t a) {  // transposed
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -551,21 +556,34 @@ prefix_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMa
 constexpr int kRing = 3;                                       // steps of 16 keys that a warp has under way
 constexpr int stage_bytes(int hd) { return 2 * 16 * hd * 2; }  // K and V
 
-// Up to 8 query heads of a kv head against keys in steps of 16.
-template <int HD, int TERMS> struct Rows {
+// Up to 8 query heads of a kv head against keys in steps of 16.  A stage holds K and V of 16 keys: rows as they lie in memory
+// (PLAIN), or by tensor copies [hd / 64][16 keys][128 B] with the 128-byte swizzle, which ldmatrix reads without bank
+// conflicts.  Of plain rows a lane reads 16 consecutive bytes (the order of the head elements in a dot product is free), with
+// two- and four-way conflicts, and puts V's pairs of keys together with byte permutes.
+template <int HD, int TERMS, bool PLAIN> struct Rows {
   static constexpr int KI = HD / 32;  // 16-byte pieces of a key a lane reads
-  uint32_t qb[TERMS][KI][2][2];       // Q^T, the second operand: head g, elements 32 i + 8 t + 4 s + {0, 1}, {2, 3}
+  // Q^T, the second operand: head g, elements 32 i + 8 t + 4 s + {0, 1}, {2, 3} (PLAIN), or 32 i + 16 s + 2 t + {0, 1}, {8, 9}
+  uint32_t qb[TERMS][KI][2][2];
   float o[HD / 16][4], m[2], l[2];    // O^T; maximum and this lane's share of the sum of heads 2 t, 2 t + 1
 
   __device__ __forceinline__ void start(const Params& p, int b, int h0, int nh) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int i = 0; i < KI; ++i) {
-      const long long at = ((long long)b * p.hq + h0 + min(g, nh - 1)) * HD + 32 * i + 8 * t;
+      const long long row = ((long long)b * p.hq + h0 + min(g, nh - 1)) * HD + 32 * i;
       if (TERMS > 1) {
-        const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at);
-        const float4 c = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at + 4);
-        float x[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+        float x[8];
+        if (PLAIN) {
+          const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + row + 8 * t);
+          const float4 c = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + row + 8 * t + 4);
+          x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = c.x; x[5] = c.y; x[6] = c.z; x[7] = c.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 a = *reinterpret_cast<const float2*>(static_cast<const float*>(p.q) + row + 8 * j + 2 * t);
+            x[2 * j] = a.x; x[2 * j + 1] = a.y;
+          }
+        }
 #pragma unroll
         for (int e = 0; e < TERMS; ++e)
 #pragma unroll
@@ -574,8 +592,14 @@ template <int HD, int TERMS> struct Rows {
             qb[e][i][s][1] = take_pair(x[4 * s + 2], x[4 * s + 3]);
           }
       } else {
-        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at);
-        qb[0][i][0][0] = a.x; qb[0][i][0][1] = a.y; qb[0][i][1][0] = a.z; qb[0][i][1][1] = a.w;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + row;
+        if (PLAIN) {
+          const uint4 a = *reinterpret_cast<const uint4*>(q + 8 * t);
+          qb[0][i][0][0] = a.x; qb[0][i][0][1] = a.y; qb[0][i][1][0] = a.z; qb[0][i][1][1] = a.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) qb[0][i][j >> 1][j & 1] = *reinterpret_cast<const uint32_t*>(q + 8 * j + 2 * t);
+        }
       }
     }
 #pragma unroll
@@ -587,30 +611,44 @@ template <int HD, int TERMS> struct Rows {
   // The first n of the 16 keys in the stage (K [16][HD], V [16][HD]).
   __device__ __forceinline__ void step(unsigned char* stage, int n, float scale_log2) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    if (n < 16) {  // rows that no key fills weigh nothing, but must not hold NaN
-      for (int i = n * (HD / 8) + lane; i < 16 * (HD / 8); i += 32) reinterpret_cast<uint4*>(stage + 16 * HD * 2)[i] = make_uint4(0, 0, 0, 0);
+    if (n < 16) {  // V's rows that no key fills weigh nothing, but must not hold NaN
+      unsigned char* v = stage + 16 * HD * 2;
+      for (int i = n * (HD / 8) + lane; i < 16 * (HD / 8); i += 32)
+        *reinterpret_cast<uint4*>(v + (PLAIN ? i * 16 : i % (HD / 8) / 8 * 2048 + i / (HD / 8) * 128 + i % 8 * 16)) = make_uint4(0, 0, 0, 0);
       __syncwarp();
     }
-    uint4 kr[2][KI], vr[4][HD / 64];  // keys g, g + 8; keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+    uint4 kr[2][KI], vr[4][HD / 64];  // PLAIN: keys g, g + 8; keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+    // swizzled: this lane's row of the 8 x 8 matrices (keys 0-7, 8-15 and the two halves of 16 elements, for V the other way)
+    const uint32_t k_row = (lane & 7) + (lane & 8), v_row = (lane & 7) + (lane >> 4 << 3);
+    const uint32_t k_at = smem_u32(stage) + k_row * 128 + ((((uint32_t)lane >> 4) ^ (k_row & 7)) << 4);
+    const uint32_t v_at = smem_u32(stage) + 16 * HD * 2 + v_row * 128 + ((((uint32_t)lane >> 3 & 1) ^ (v_row & 7)) << 4);
+    if (PLAIN)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int i = 0; i < KI; ++i) kr[j][i] = *reinterpret_cast<const uint4*>(stage + (g + 8 * j) * HD * 2 + 16 * t + 64 * i);
+        for (int i = 0; i < KI; ++i) kr[j][i] = *reinterpret_cast<const uint4*>(stage + (g + 8 * j) * HD * 2 + 16 * t + 64 * i);
     // the hardware's sums drop bits: the small terms in chains of their own
     float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[TERMS > 1 ? TERMS - 1 : 1][4] = {};
 #pragma unroll
-    for (int e = TERMS - 1; e >= 0; --e)
+    for (int i = 0; i < KI; ++i)
 #pragma unroll
-      for (int i = 0; i < KI; ++i) {
-        float* c = e > 0 ? s2[e - 1] : s;
-        mma16816(c, kr[0][i].x, kr[1][i].x, kr[0][i].y, kr[1][i].y, qb[e][i][0][0], qb[e][i][0][1]);
-        mma16816(c, kr[0][i].z, kr[1][i].z, kr[0][i].w, kr[1][i].w, qb[e][i][1][0], qb[e][i][1][1]);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t a[4];
+        if (PLAIN) {
+          a[0] = h ? kr[0][i].z : kr[0][i].x; a[1] = h ? kr[1][i].z : kr[1][i].x;
+          a[2] = h ? kr[0][i].w : kr[0][i].y; a[3] = h ? kr[1][i].w : kr[1][i].y;
+        } else {  // elements 32 i + 16 h .. + 15: pieces 4 i + 2 h and the next
+          ldsm(a, (k_at ^ ((4 * i + 2 * h) % 8 << 4)) + (4 * i + 2 * h) / 8 * 2048);
+        }
+#pragma unroll
+        for (int e = TERMS - 1; e >= 0; --e) mma16816(e > 0 ? s2[e - 1] : s, a[0], a[1], a[2], a[3], qb[e][i][h][0], qb[e][i][h][1]);
       }
+    if (PLAIN)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int c = 0; c < HD / 64; ++c)
-        vr[j][c] = *reinterpret_cast<const uint4*>(stage + (16 + 2 * t + (j & 1) + 8 * (j >> 1)) * HD * 2 + 16 * g + 128 * c);
+        for (int c = 0; c < HD / 64; ++c)
+          vr[j][c] = *reinterpret_cast<const uint4*>(stage + (16 + 2 * t + (j & 1) + 8 * (j >> 1)) * HD * 2 + 16 * g + 128 * c);
     // s: (key g, heads 2t, 2t+1), (key g + 8, heads 2t, 2t+1)
     float al[2], pr[4];
 #pragma unroll
@@ -649,8 +687,15 @@ template <int HD, int TERMS> struct Rows {
     };
 #pragma unroll
     for (int e = 0; e < HD / 16; ++e) {
-      const int lo = HD == 128 ? e : 2 * e, hi = HD == 128 ? e + 8 : 2 * e + 1;
-      const uint32_t a0 = take(0, lo), a1 = take(0, hi), a2 = take(2, lo), a3 = take(2, hi);
+      uint32_t a0, a1, a2, a3;
+      if (PLAIN) {
+        const int lo = HD == 128 ? e : 2 * e, hi = HD == 128 ? e + 8 : 2 * e + 1;
+        a0 = take(0, lo); a1 = take(0, hi); a2 = take(2, lo); a3 = take(2, hi);
+      } else {  // elements 16 e .. + 15: pieces 2 e and the next, transposed
+        uint32_t a[4];
+        ldsm_t(a, (v_at ^ (2 * e % 8 << 4)) + 2 * e / 8 * 2048);
+        a0 = a[0]; a1 = a[1]; a2 = a[2]; a3 = a[3];
+      }
       if (TERMS == 1) {
         mma16816(o[e], a0, a1, a2, a3, pb[0][0], pb[0][1]);
       } else {  // this step's sum apart from the total, which is added to with rounding
@@ -672,6 +717,7 @@ template <int HD, int TERMS> struct Rows {
   }
   // o[e][x] belongs to head 2 t + (x & 1) and this element: rows g of the product are the low ones, rows g + 8 the high ones
   static __device__ __forceinline__ int element(int e, int x, int g) {
+    if (!PLAIN) return 16 * e + (x < 2 ? 0 : 8) + g;
     return HD == 128 ? (x < 2 ? 0 : 64) + g * 8 + e : g * 8 + 2 * e + (x < 2 ? 0 : 1);
   }
 };
@@ -772,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, TERMS == 1 ? 3 : 2) rows_kernel(cons
       const int k = key0 + i * key_step;
       if (k < nkeys) fetch<HD>(p, ring + i * stage_bytes(HD), &bar[i], b, kh, p.P, k, min(16, nkeys - k), pol);
     }
-  Rows<HD, TERMS> r;
+  Rows<HD, TERMS, true> r;
   r.start(p, b, h0, nh);
   __syncwarp();  // the barriers are set up
   bool ok = true;
@@ -857,52 +903,55 @@ __global__ void __launch_bounds__(kThreads, TERMS == 1 ? 3 : 2) rows_kernel(cons
 // ---------------------------------------------------------------------------------------------
 // parts kernel: the sequences' own keys, beside the prefix kernel
 // ---------------------------------------------------------------------------------------------
-// A block is one warp with a run of `own_run` keys of a (sequence, kv head, 8 query heads): small enough that two of them
-// find room on an SM beside a block of the prefix kernel, and nine when that is done.  Its part: O [8 heads][hd] and (maximum,
-// sum) of the 8 heads.  The first runs of all pairs come first, the longest by their lengths.
+// A block is one warp with a run of `own_run` keys of a (sequence, kv head, 8 query heads): small enough that three of them
+// find room on an SM beside a block of the prefix kernel, and twelve when that is done.  Its part: O [8 heads][hd] and
+// (maximum, sum) of the 8 heads.  The first runs of all pairs come first.  Two stages: a third costs a block's place (256
+// sequences: 87 us against 89); two warps on four stages gain nothing (90), three on six are slower (92).
+constexpr int kPartRing = 2;
+
 template <int HD, int TERMS>
-__global__ void __launch_bounds__(32, 12) parts_kernel(const __grid_constant__ Params p) {
-  extern __shared__ __align__(128) unsigned char ring[];
-  __shared__ __align__(8) uint64_t bar[kRing];
+__global__ void __launch_bounds__(32, 12) parts_kernel(const __grid_constant__ Params p, const __grid_constant__ PrefixMaps maps) {
+  extern __shared__ __align__(1024) unsigned char ring_raw[];
+  unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(ring_raw) + 1023) & ~(uintptr_t)1023);
+  static_assert(kPartRing * stage_bytes(HD) >= kHeads * (HD + 4) * 4, "the warp's sums fit over the ring");
+  __shared__ __align__(8) uint64_t bar[kPartRing];
   const int lane = threadIdx.x, g = lane >> 2, t = lane & 3;
   const int pairs = p.B * p.hkv * p.hblocks, run = blockIdx.x / pairs, pair = blockIdx.x - run * pairs;
   const int hb = pair % p.hblocks, kh = pair / p.hblocks % p.hkv, b = pair / p.hblocks / p.hkv;
   const int len = __ldg(p.lens + b), k0 = run * p.own_run, k1 = len > p.max_seq ? 0 : min(len, k0 + p.own_run);
-  pdl_trigger();  // the join kernel may come in when the last of these blocks has started
   if (k0 < k1) {  // else no part: the length says so
-    if (lane == 0) {
-      for (int i = 0; i < kRing; ++i) mbar_init(&bar[i], 1);
-      fence_mbar_init();
-    }
-    __syncwarp();
-    const uint64_t pol = l2_evict_first_policy();
-    const long long at = (((long long)b * p.hkv + kh) * p.max_seq + k0) * HD;
-    const __nv_bfloat16 *ks = p.kc + at, *vs = p.vc + at;
-    auto issue = [&](int st, int k) {  // keys k .. of the run
-      const uint32_t bytes = min(16, k1 - k0 - k) * HD * 2;
-      mbar_arrive_expect_tx(&bar[st], 2 * bytes);
-      bulk_g2s(ring + st * stage_bytes(HD), ks + (long long)k * HD, bytes, &bar[st], pol);
-      bulk_g2s(ring + st * stage_bytes(HD) + 16 * HD * 2, vs + (long long)k * HD, bytes, &bar[st], pol);
+    const int steps = (k1 - k0 + 15) / 16;
+    auto issue = [&](int i) {  // step i; keys behind the sequence's are not used
+      unsigned char* dst = ring + i % kPartRing * stage_bytes(HD);
+      uint64_t* full = &bar[i % kPartRing];
+      mbar_arrive_expect_tx(full, stage_bytes(HD));
+#pragma unroll
+      for (int h = 0; h < HD / 64; ++h) {
+        tma3(dst + h * 2048, &maps.k, h * 64, k0 + 16 * i, b * p.hkv + kh, full);
+        tma3(dst + 16 * HD * 2 + h * 2048, &maps.v, h * 64, k0 + 16 * i, b * p.hkv + kh, full);
+      }
     };
-    if (lane == 0)
-      for (int i = 0; i < kRing; ++i)
-        if (16 * i < k1 - k0) issue(i, 16 * i);
-    Rows<HD, TERMS> r;
-    r.start(p, b, kh * p.gq + hb * kHeads, min(kHeads, p.gq - hb * kHeads));
-    bool ok = true;
-    int st = 0;
-    uint32_t ph = 0;
-    for (int k = 0; k < k1 - k0; k += 16) {
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[st], ph)) != 0;
-      r.step(ring + st * stage_bytes(HD), min(16, k1 - k0 - k), p.scale_log2);
-      __syncwarp();  // every lane has read the stage
-      if (lane == 0 && ok && k + 16 * kRing < k1 - k0) issue(st, k + 16 * kRing);
-      if (++st == kRing) { st = 0; ph ^= 1; }
+    if (lane == 0) {
+      for (int i = 0; i < kPartRing; ++i) mbar_init(&bar[i], 1);
+      fence_mbar_init();
+      for (int i = 0; i < kPartRing && i < steps; ++i) issue(i);
     }
+    Rows<HD, TERMS, false> r;
+    r.start(p, b, kh * p.gq + hb * kHeads, min(kHeads, p.gq - hb * kHeads));
+    __syncwarp();  // the barriers are set up
+    bool ok = true;
+    for (int i = 0; i < steps; ++i) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[i % kPartRing], i / kPartRing & 1)) != 0;
+      r.step(ring + i % kPartRing * stage_bytes(HD), min(16, k1 - k0 - 16 * i), p.scale_log2);
+      __syncwarp();  // every lane has read the stage
+      if (lane == 0 && ok && i + kPartRing < steps) issue(i + kPartRing);
+    }
+    if (!ok)  // a wait gave up: the copies in flight land before the block leaves
+      for (int i = 0; i < kPartRing; ++i)
+        for (int parity = 0; parity < 2; ++parity) mbar_wait_bounded(&bar[i], parity, 10000000ull);
     r.join_sums();
     const size_t part = (size_t)pair * p.own_runs + run;
-    __syncwarp();  // the ring is read: O goes through it, to be written in rows
-    float* so = reinterpret_cast<float*>(ring);
+    float* so = reinterpret_cast<float*>(ring);  // O goes through the ring, to be written in rows
 #pragma unroll
     for (int e = 0; e < HD / 16; ++e)
 #pragma unroll
@@ -914,8 +963,6 @@ __global__ void __launch_bounds__(32, 12) parts_kernel(const __grid_constant__ P
     if (g == 0)
 #pragma unroll
       for (int j = 0; j < 2; ++j) p.own_ml[part * kHeads + 2 * t + j] = make_float2(r.m[j], ok ? r.l[j] : NAN);  // NaN: a wait gave up
-    if (!ok)  // the copies in flight land before the block leaves
-      for (int i = 0; i < kRing; ++i) mbar_wait_bounded(&bar[(st + i) % kRing], ph ^ (st + i >= kRing), 10000000ull);
   }
   // One block ends only after the prefix kernel, so that the end of this kernel is the end of both; the others make room.
   if (blockIdx.x == gridDim.x - 1) pdl_wait();
@@ -1052,10 +1099,10 @@ void prefix_geometry(int rows, int hkv, int P, int ns, int sms, Params* p) {
   p->n_cta = (int)(total < sms ? total : sms);
 }
 size_t part_rows(const Params& p, int ns) { return ((size_t)p.n_cta + p.units) * ns * kTile; }
-// Runs of a sequence's own keys: 4096 parts in all where the batch is smaller, 16 of a sequence at most.
+// Runs of a sequence's own keys: 4096 in all where the batch is smaller, 16 of a sequence at most.
 int most_own_runs(long long pairs) { return pairs >= 4096 ? 1 : 4096 / pairs < 16 ? (int)(4096 / pairs) : 16; }
 
-cudaError_t encode_map(CUtensorMap* out, const void* base, int hd, int P, int cap, int hkv) {
+cudaError_t encode_map(CUtensorMap* out, const void* base, int hd, int P, long long cap, int hkv, int rows) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   static std::mutex mu;
   {
@@ -1069,10 +1116,11 @@ cudaError_t encode_map(CUtensorMap* out, const void* base, int hd, int P, int ca
       encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
   }
-  // (element, key, kv head); the key dimension ends at P: keys beyond it are zeros in shared memory
+  // (element, key, kv head), box 64 elements x `rows` keys; the key dimension ends at P: keys beyond it are zeros in shared
+  // memory
   const cuuint64_t dim[3] = {(cuuint64_t)hd, (cuuint64_t)P, (cuuint64_t)hkv};
   const cuuint64_t stride[2] = {(cuuint64_t)hd * 2, (cuuint64_t)cap * hd * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)kTile, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
   const cuuint32_t one[3] = {1, 1, 1};
   const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dim, stride, box, one,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1095,6 +1143,8 @@ cudaError_t launch(Params& p, void* workspace, cudaStream_t s) {
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(rows_kernel<HD, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  rows_smem(kWarps, HD));
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(parts_kernel<HD, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPartRing * stage_bytes(HD) + 1024);
       // all of the SM's memory as shared memory, so that blocks of both kernels fit beside one another
       if (e == cudaSuccess) e = cudaFuncSetAttribute(prefix_kernel<HD, TERMS>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
       if (e == cudaSuccess) e = cudaFuncSetAttribute(parts_kernel<HD, TERMS>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
@@ -1142,8 +1192,8 @@ cudaError_t launch(Params& p, void* workspace, cudaStream_t s) {
   p.own_runs = p.max_seq > 0 ? (int)((p.max_seq + p.own_run - 1) / p.own_run) : 1;
   p.parts = p.own_runs + p.n_cta;
   PrefixMaps maps;
-  e = encode_map(&maps.k, p.pk, HD, p.P, (int)p.prefix_cap, p.hkv);
-  if (e == cudaSuccess) e = encode_map(&maps.v, p.pv, HD, p.P, (int)p.prefix_cap, p.hkv);
+  e = encode_map(&maps.k, p.pk, HD, p.P, p.prefix_cap, p.hkv, kTile);
+  if (e == cudaSuccess) e = encode_map(&maps.v, p.pv, HD, p.P, p.prefix_cap, p.hkv, kTile);
   if (e != cudaSuccess) return e;
   // Three kernels in one stream, each allowed to start beside the one before: the prefix kernel waits for what came before
   // the call, and only then lets the parts kernel in beside it, which ends after it; the join kernel waits for that.
@@ -1154,8 +1204,11 @@ cudaError_t launch(Params& p, void* workspace, cudaStream_t s) {
   if (p.max_seq > 0) {
     cfg.gridDim = dim3((unsigned)(pairs * p.own_runs));
     cfg.blockDim = dim3(32);
-    cfg.dynamicSmemBytes = (size_t)kRing * stage_bytes(HD);
-    if ((e = cudaLaunchKernelEx(&cfg, parts_kernel<HD, TERMS>, p)) != cudaSuccess) return e;
+    cfg.dynamicSmemBytes = (size_t)kPartRing * stage_bytes(HD) + 1024;
+    e = encode_map(&maps.k, p.kc, HD, (int)p.max_seq, p.max_seq, p.B * p.hkv, 16);
+    if (e == cudaSuccess) e = encode_map(&maps.v, p.vc, HD, (int)p.max_seq, p.max_seq, p.B * p.hkv, 16);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, parts_kernel<HD, TERMS>, p, maps);
+    if (e != cudaSuccess) return e;
   }
   cfg.gridDim = dim3((unsigned)pairs);
   cfg.blockDim = dim3(kJoin);
