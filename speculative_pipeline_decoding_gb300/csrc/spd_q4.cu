@@ -556,7 +556,8 @@ cudaError_t launch_gw(const Params& p, int group, dim3 grid, size_t smem, cudaSt
 }
 
 // How the work is cut, for one block an SM: sets mb, chunk and batch; returns the operand tiles of a warp.
-//   mb: at most 48 operand columns (6 tiles of accumulators), in even shares.
+//   mb: at most 48 operand columns (6 tiles of accumulators), in even shares.  More vectors in a pass read the weights less
+//       often; 6 tiles are what 128 registers hold beside the records ahead.
 //   batch: the tiles of a block, as far as 96 KB of parts hold.
 //   chunk: all columns if they fit the rest of 224 KB, else even shares of them.
 int plan(Params* p, int sms) {

@@ -12,7 +12,8 @@
 // A warp takes a token, or a share of its heads where there are few tokens.  A lane keeps its place within the heads (16
 // bytes of each side of its pairs), so that it needs the cosines and sines of the same pairs for all heads, in registers:
 // they are formed once, spread over the lanes, and handed round through the warp's own shared memory.  No block barrier, and
-// four heads' loads under way before the first is used.
+// four heads' loads under way before the first is used.  8192 tokens of those heads: bf16 36 us (82% of the measured copy
+// bandwidth), fp32 61 us (89%); a block a token with two of its heads' loads under way took 55.
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -145,6 +146,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 }
 
 // Element by element, for strides, addresses or a half of the rotated part that do not allow whole vectors: a block a token.
+// 8192 bf16 tokens with 122 of 128 elements rotated: 91 us, against 36 by whole vectors.
 template <typename X, typename C, bool INTER>
 __global__ void __launch_bounds__(kScalarThreads) rope_scalar_kernel(const __grid_constant__ Params p) {
   __shared__ float2 trig[2][SPD_ROPE_MAX_PAIRS];
@@ -206,6 +208,7 @@ cudaError_t launch(Params& p, bool vec, bool inter, cudaStream_t s) {
     return inter ? cudaLaunchKernelEx(&cfg, rope_scalar_kernel<X, C, true>, p) : cudaLaunchKernelEx(&cfg, rope_scalar_kernel<X, C, false>, p);
   }
   // shares of a token: kSteps steps each, whose loads are under way together, as far as the GPU's warps (24 an SM) go
+  // (193 tokens of 28 + 2 x 4 heads: 4.0 us, against 5.7 with a share for every step, whose cosines are then formed four times)
   const int per_head = p.hd / (2 * WTraits<X>::kVec), hps = 32 / per_head, steps = (p.hq + 2 * p.hkv + hps - 1) / hps;
   const int warps = 24 * sms, wpb = kThreads / 32;
   const int share = warps / p.T;
