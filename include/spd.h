@@ -402,8 +402,8 @@ int spd_rope_init(spd_rope* out, int32_t head_dim, int32_t rot_dim, int32_t layo
  *   sequence lies outside 0..n_seqs-1 is rotated but not appended (padding); other rows of the cache
  *   are left as they were.  No two tokens of a call may name the same row.
  * n_heads or n_kv_heads may be 0 (their pointers are ignored); T = 0 does nothing.  Angles are exact
- * at any position (64-bit fixed point), products are fp32.  Any alignment of the elements' own size
- * works; 16-byte aligned rows (and rot_dim / 2 a multiple of 16 bytes in the half layout) are faster. */
+ * at any position (64-bit fixed point), products are fp32.  Pointers must be aligned to their elements
+ * (SPD_EINVAL else); 16-byte aligned rows (and rot_dim / 2 a multiple of 16 bytes in the half layout) are faster. */
 int spd_rope_append(const spd_rope* rope, const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
                     const void* k, int64_t k_stride, const void* v, int64_t v_stride, int32_t x_dtype,
                     const int32_t* pos, int32_t T, int32_t n_heads, int32_t n_kv_heads, void* k_cache,

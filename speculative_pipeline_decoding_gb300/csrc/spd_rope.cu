@@ -280,6 +280,11 @@ extern "C" int spd_rope_append(const spd_rope* rope, const void* q, int64_t q_st
     return bad("spd_rope_append: bad sizes");
   if (T == 0) return SPD_OK;
   const int hd = rope->head_dim;
+  const size_t xe = x_dtype == SPD_DTYPE_F32 ? 4 : 2, ce = cache_dtype == SPD_DTYPE_F32 ? 4 : 2;
+  auto off = [](const void* ptr, size_t n) { return reinterpret_cast<uintptr_t>(ptr) % n != 0; };
+  if (off(pos, 4) || (n_heads && (off(q, xe) || off(q_out, xe))) ||
+      (n_kv_heads && (off(k, xe) || off(v, xe) || off(k_cache, ce) || off(v_cache, ce) || off(slot, 4) || off(seq, 4))))
+    return bad("spd_rope_append: a pointer is not aligned to its elements");
   const long long qw = (long long)n_heads * hd, kw = (long long)n_kv_heads * hd;
   if (!pos || (n_heads && (!q || !q_out))) return bad("spd_rope_append: NULL pointer");
   if (n_heads && (q_stride < qw || q_out_stride < qw)) return bad("spd_rope_append: a row stride is below the row's length");

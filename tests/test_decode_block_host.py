@@ -75,18 +75,21 @@ def _append(L, plan, **kw):
 
 @pytest.mark.parametrize("bad", [dict(q=None), dict(qo=None), dict(pos=None), dict(k=None), dict(v=None), dict(kc=None), dict(vc=None),
                                  dict(slot=None), dict(qs=1023), dict(qos=1000), dict(ks=255), dict(vs=0), dict(qos=2048), dict(xdt=2),
-                                 dict(cdt=-1), dict(T=-1), dict(hq=-1), dict(hq=0, hkv=0), dict(hkv=-2), dict(n_seqs=0), dict(max_seq=0)])
+                                 dict(cdt=-1), dict(T=-1), dict(q=FAKE + 2), dict(qo=FAKE + 1), dict(k=FAKE + 2), dict(v=FAKE + 3),
+                                 dict(xdt=1, q=FAKE + 1), dict(kc=FAKE + 1), dict(vc=FAKE + 2, cdt=0), dict(pos=FAKE + 2), dict(slot=FAKE + 1), dict(seq=FAKE + 2), dict(hq=-1), dict(hq=0, hkv=0), dict(hkv=-2), dict(n_seqs=0), dict(max_seq=0)])
 def test_rope_append_refuses(L, bad):
     from speculative_pipeline_decoding_gb300.binding import Rope
-    assert _append(L, Rope(128)._at, **bad) == -1
+    plan = Rope(128)
+    assert _append(L, ctypes.addressof(plan.c), **bad) == -1
     assert "spd_rope_append" in _message(L)
 
 
 def test_rope_append_refuses_foreign_plans_and_takes_no_tokens(L):
     from speculative_pipeline_decoding_gb300.binding import Rope, spd_rope
+    empty, plan = spd_rope(), Rope(128)
     assert _append(L, None) == -1
-    assert _append(L, ctypes.addressof(spd_rope())) == -1
-    assert _append(L, Rope(128)._at, T=0) == 0
+    assert _append(L, ctypes.addressof(empty)) == -1
+    assert _append(L, ctypes.addressof(plan.c), T=0) == 0
 
 
 def test_q4_sizes(L):
