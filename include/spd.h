@@ -436,9 +436,9 @@ int spd_q4_pack(const uint8_t* codes, const void* scales, const uint8_t* zeros, 
  * x [M] rows of cols elements and y [M] rows of `rows` elements, both in x_dtype, row m starting at
  * m * stride.  All groups share cols, group, scale_dtype and has_zeros.  fp32 vectors are multiplied
  * exactly (three bf16 terms each), bf16 vectors as they are (normalised ones as two bf16 terms);
- * sums are fp32 in an order fixed by the sizes.  Groups must not write the same y, nor
- * over an x.  SPD_EINVAL on bad
- * sizes, NULL pointers, or unaligned ones (packed weights 16 bytes, x, y and nw their element). */
+ * sums are fp32 in an order fixed by the sizes.  Groups must not write the same y, nor over an x.
+ * SPD_EINVAL on bad sizes, NULL pointers, unaligned ones (packed weights 16 bytes, x, y and nw their
+ * element), or y_g = x_g. */
 typedef struct spd_q4_group {
   const void* w;     /* spd_q4_pack's output */
   const void* x;
@@ -458,7 +458,7 @@ int spd_q4_gemv(const spd_q4_group* groups, int32_t G, int32_t M, int32_t cols, 
  *   prefix_k, prefix_v bf16 [n_kv_heads][prefix_cap][hd]; k_cache, v_cache bf16 [B][n_kv_heads][max_seq][hd];
  *   lens int32 [B], read on the device (a captured call follows them); lse fp32 [B][n_heads] or NULL.
  * hd 64 or 128; n_heads at most 1024; B 0..4096 (0: nothing to do); 0 <= prefix_len <= prefix_cap (0: the prefix pointers may be NULL); max_seq >= 0
- * (0: no sequence has keys of its own, the cache pointers and lens may be NULL).  Rows of the caches from
+ * (0: no sequence has keys of its own, the cache pointers and lens are ignored).  Rows of the caches from
  * prefix_len or lens[b] on are not used, whatever they hold.  A sequence without any key gets out = 0 and
  * lse = -inf; one whose lens[b] lies outside 0..max_seq gets NaN.  Every pointer 16-byte aligned (lens
  * and lse 4).  `workspace` (>= spd_shared_prefix_attention_workspace_bytes, 16-byte aligned) holds

@@ -480,6 +480,8 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
 # ---------------------------------------------------------------------------
 _DT = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 _I32, _BF16 = torch.int32, torch.bfloat16
+_INT_MAX = 0x7FFFFFFF
+_addressof = ctypes.addressof
 # the short forms of torch.cuda.current_stream(device).cuda_stream and torch.cuda.current_device()
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torch.cuda.current_stream(device).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -546,7 +548,6 @@ class Rope:
         self.rot_dim = self.head_dim if rot_dim is None else int(rot_dim)
         _check(lib().spd_rope_init(ctypes.addressof(self.c), self.head_dim, self.rot_dim, ROPE_LAYOUTS[layout], float(theta),
                                    ROPE_SCALINGS[scaling], float(factor), int(original_context)))
-        self._at = ctypes.addressof(self.c)
 
 
 def rope_append(rope: Rope, q: Optional[torch.Tensor], q_out: Optional[torch.Tensor], pos: torch.Tensor, k=None, v=None,
@@ -597,18 +598,33 @@ def rope_append(rope: Rope, q: Optional[torch.Tensor], q_out: Optional[torch.Ten
             sqp = _ints("seq", seq, T)
     elif v is not None or k_cache is not None or v_cache is not None or slot is not None or seq is not None:
         raise _bad("v, the caches, slot and seq belong to k")
-    _call(lib().spd_rope_append, dev, (rope._at, qp, qs, qo, qos, kp, ks, vp, vs, _DT[dt], pos.data_ptr(), T, hq, hkv, kcp, vcp,
+    if T > _INT_MAX or n_seqs > _INT_MAX or max_seq > _INT_MAX:
+        raise _bad("more tokens or cache rows than 32 bits count")
+    _call(lib().spd_rope_append, dev, (_addressof(rope.c), qp, qs, qo, qos, kp, ks, vp, vs, _DT[dt], pos.data_ptr(), T, hq, hkv, kcp, vcp,
                                        _DT[cdt], sp, sqp, n_seqs, max_seq, _stream_of(dev, stream)))
 
 
 class Q4Matrix:
-    """A [rows, cols] matrix of 4-bit codes with group scales, laid out for :func:`q4_gemv` (see :func:`q4_pack`)."""
+    """A [rows, cols] matrix of 4-bit codes with group scales, laid out for :func:`q4_gemv` (see :func:`q4_pack`).
+
+    ``packed`` is the buffer; a matrix read back from a file, or moved to another GPU, is a new object around it."""
 
     def __init__(self, packed: torch.Tensor, rows: int, cols: int, group: int, scale_dtype: torch.dtype, has_zeros: bool):
-        self.packed, self.rows, self.cols, self.group = packed, rows, cols, group
-        self.scale_dtype, self.has_zeros = scale_dtype, has_zeros
+        if packed.dtype is not torch.uint8 or packed.dim() != 1 or not packed.is_contiguous() or scale_dtype not in _DT:
+            raise _bad("packed must be a contiguous uint8 vector, scale_dtype fp32 or bf16")
+        big = max(rows, cols, group) > _INT_MAX
+        need = 0 if big else lib().spd_q4_packed_bytes(rows, cols, group, _DT[scale_dtype], int(has_zeros))
+        if not need or packed.numel() != need:
+            raise _bad("packed does not hold a matrix of these sizes")
+        self._packed, self._rows = packed, rows
         self._kind = (cols, group, _DT[scale_dtype], int(has_zeros))
-        self._ptr, self._dev = packed.data_ptr(), packed.get_device()
+        self.scale_dtype = scale_dtype
+
+    packed = property(lambda self: self._packed)
+    rows = property(lambda self: self._rows)
+    cols = property(lambda self: self._kind[0])
+    group = property(lambda self: self._kind[1])
+    has_zeros = property(lambda self: bool(self._kind[3]))
 
 
 def q4_quantize(w: torch.Tensor, group: int = 128, symmetric: bool = True, scale_dtype: torch.dtype = torch.bfloat16, stream=None):
@@ -656,29 +672,32 @@ def q4_gemv(Ws: Sequence[Q4Matrix], xs: Sequence[torch.Tensor], ys: Sequence[tor
     """ys[g][m] = Ws[g] @ (rmsnorm(xs[g][m]) * norm_weight if norm_weight is given else xs[g][m]) for up to 32 vectors m.
 
     xs [M, cols] and ys [M, rows], or one vector [cols] and [rows]; fp32 or bf16, all in one dtype; rows contiguous, any
-    row stride.  The matrices share columns, group, scale dtype and the presence of zero points."""
+    row stride.  The matrices share columns, group, scale dtype and the presence of zero points.  No y may lie over an x or
+    over another y."""
     G = len(Ws)
     if G < 1 or G > 34 or len(xs) != G or len(ys) != G:
         raise _bad("q4_gemv takes 1 to 34 matrices, with a vector and an output each")
-    kind, dev, x0 = Ws[0]._kind, Ws[0]._dev, xs[0]
+    kind, dev, x0 = Ws[0]._kind, Ws[0]._packed.get_device(), xs[0]
     cols, dt = kind[0], x0.dtype
     shape = x0.shape
     nd = len(shape)
     if dt not in _DT or nd not in (1, 2):
         raise _bad("xs must be fp32 or bf16, [M, cols] or [cols]")
     M = 1 if nd == 1 else shape[0]
+    if dev < 0 or M > 32:
+        raise _bad("q4_gemv takes matrices on the GPU and up to 32 vectors")
     words = []  # the fields of spd_q4_group, 8 bytes each (rows and reserved share one)
     for W, x, y in zip(Ws, xs, ys):
         if W._kind != kind:
             raise _bad("the matrices of a call share columns, group, scale dtype and zero points")
-        sx, sy = x.stride(), y.stride()
-        if x.dtype is not dt or y.dtype is not dt or x.shape != shape or y.shape != (shape[:-1] + (W.rows,)):
+        sx, sy, w, rows = x.stride(), y.stride(), W._packed, W._rows
+        if x.dtype is not dt or y.dtype is not dt or x.shape != shape or y.shape != (shape[:-1] + (rows,)):
             raise _bad(f"xs must be [M, {cols}] and ys [M, rows of the matrix], in one dtype, with one M")
-        if shape[-1] != cols or sx[-1] != 1 or (sy[-1] != 1 and W.rows > 1):
+        if shape[-1] != cols or sx[-1] != 1 or (sy[-1] != 1 and rows > 1):
             raise _bad(f"x and y rows must be contiguous, x of {cols} columns")
-        if x.get_device() != dev or y.get_device() != dev or W._dev != dev:
+        if x.get_device() != dev or y.get_device() != dev or w.get_device() != dev:
             raise _bad("tensors must live on one GPU")
-        words += (W._ptr, x.data_ptr(), y.data_ptr(), sx[0] if M > 1 else 0, sy[0] if M > 1 else 0, W.rows)
+        words += (w.data_ptr(), x.data_ptr(), y.data_ptr(), sx[0] if M > 1 else 0, sy[0] if M > 1 else 0, rows)
     nw = None
     if norm_weight is not None:
         if (norm_weight.dtype is not torch.float32 or norm_weight.shape != (cols,) or not norm_weight.is_contiguous()
@@ -694,6 +713,8 @@ def q4_gemv(Ws: Sequence[Q4Matrix], xs: Sequence[torch.Tensor], ys: Sequence[tor
 
 def shared_prefix_attention_workspace_bytes(B: int, n_heads: int, n_kv_heads: int, head_dim: int, prefix_len: int) -> int:
     """Workspace of a call, or 0 for sizes that it refuses."""
+    if max(B, n_heads, n_kv_heads, head_dim, prefix_len) > _INT_MAX:
+        return 0
     return int(lib().spd_shared_prefix_attention_workspace_bytes(B, n_heads, n_kv_heads, head_dim, prefix_len))
 
 
@@ -713,6 +734,8 @@ def shared_prefix_attention(q: torch.Tensor, prefix_k: Optional[torch.Tensor], p
     dev = q.get_device()
     _same_device(dev, out, workspace)
     B, hq, hd = shape
+    if prefix_len > (0 if prefix_k is None else prefix_k.size(1)):
+        raise _bad("the prefix is longer than prefix_k")
     pkp = pvp = kcp = vcp = lp = ep = None
     hkv = cap = max_seq = 0
     if prefix_k is not None:
@@ -737,6 +760,8 @@ def shared_prefix_attention(q: torch.Tensor, prefix_k: Optional[torch.Tensor], p
         kcp, vcp, lp = k_cache.data_ptr(), v_cache.data_ptr(), _ints("lens", lens, B)
     elif v_cache is not None or lens is not None:
         raise _bad("v_cache and lens belong to k_cache")
+    if cap > _INT_MAX or max_seq > _INT_MAX:
+        raise _bad("more cache rows than 32 bits count")
     if not hkv:
         raise _bad("neither a prefix nor caches")
     if lse is not None:

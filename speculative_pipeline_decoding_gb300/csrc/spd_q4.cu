@@ -645,10 +645,10 @@ extern "C" int spd_q4_gemv(const spd_q4_group* groups, int32_t G, int32_t M, int
   long long tiles = 0;
   for (int g = 0; g < G; ++g) {
     const spd_q4_group& s = groups[g];
-    if (s.rows < 1 || !s.w || !s.x || !s.y || !q4::aligned(s.w, 16) || !q4::aligned(s.x, esz) || !q4::aligned(s.y, esz) ||
+    if (s.rows < 1 || !s.w || !s.x || !s.y || s.x == s.y || !q4::aligned(s.w, 16) || !q4::aligned(s.x, esz) || !q4::aligned(s.y, esz) ||
         (M > 1 && (s.x_stride < cols || s.y_stride < s.rows))) {
       char msg[128];
-      snprintf(msg, sizeof(msg), "spd_q4_gemv: group %d: NULL or unaligned pointer, no rows, or a stride below the row", g);
+      snprintf(msg, sizeof(msg), "spd_q4_gemv: group %d: NULL or unaligned pointer, y over x, no rows, or a stride below the row", g);
       return spd_internal_fail(SPD_EINVAL, msg);
     }
     q4::Group& d = p.g[g];

@@ -115,7 +115,7 @@ def test_q4_quantize_and_pack_refuse(L):
 
 def _gemv(L, groups=1, group=None, **kw):
     from speculative_pipeline_decoding_gb300.binding import spd_q4_group
-    g = dict(w=FAKE, x=FAKE, y=FAKE, x_stride=256, y_stride=64, rows=64, reserved=0)
+    g = dict(w=FAKE, x=FAKE, y=2 * FAKE, x_stride=256, y_stride=64, rows=64, reserved=0)
     g.update(group or {})
     arr = (spd_q4_group * max(1, groups))(*[spd_q4_group(**g) for _ in range(max(1, groups))])
     a = dict(G=groups, M=2, cols=256, group=128, sdt=1, z=0, xdt=0, nw=None, eps=1e-6)
@@ -126,7 +126,7 @@ def _gemv(L, groups=1, group=None, **kw):
 @pytest.mark.parametrize("bad", [dict(groups=0), dict(groups=35), dict(M=0), dict(M=33), dict(cols=100), dict(cols=0), dict(cols=65536),
                                  dict(group=dict(w=None)), dict(group=dict(x=None)), dict(group=dict(y=None)), dict(group=dict(rows=0)),
                                  dict(group=dict(w=FAKE + 8)), dict(group=dict(x=FAKE + 2)), dict(group=dict(y=FAKE + 1)), dict(group=dict(x_stride=255)),
-                                 dict(group=dict(y_stride=63)), dict(sdt=2), dict(xdt=3), dict(nw=FAKE + 2), dict(nw=FAKE, eps=-1.0),
+                                 dict(group=dict(y_stride=63)), dict(group=dict(y=FAKE, x=FAKE)), dict(sdt=2), dict(xdt=3), dict(nw=FAKE + 2), dict(nw=FAKE, eps=-1.0),
                                  dict(nw=FAKE, eps=math.nan)])
 def test_q4_gemv_refuses(L, bad):
     assert _gemv(L, **bad) == -1
@@ -135,7 +135,7 @@ def test_q4_gemv_refuses(L, bad):
 
 def test_q4_gemv_refuses_other_group_sizes(L):
     from speculative_pipeline_decoding_gb300.binding import spd_q4_group
-    arr = (spd_q4_group * 1)(spd_q4_group(FAKE, FAKE, FAKE, 256, 64, 64, 0))
+    arr = (spd_q4_group * 1)(spd_q4_group(FAKE, FAKE, 2 * FAKE, 256, 64, 64, 0))
     for n in (0, 16, 48, 256):
         assert L.spd_q4_gemv(ctypes.addressof(arr), 1, 1, 256, n, 1, 0, 0, None, 1e-6, None) == -1
     assert L.spd_q4_gemv(None, 1, 1, 256, 128, 1, 0, 0, None, 1e-6, None) == -1
@@ -178,3 +178,44 @@ def test_binding_refuses_tensors_off_the_gpu(L):
     kv = torch.zeros(2, 4, 128, dtype=torch.bfloat16)
     with pytest.raises(spd.SpdError):
         spd.shared_prefix_attention(q, kv, kv, 4, None, None, None, q.clone(), torch.zeros(1 << 16, dtype=torch.uint8))
+
+
+def test_packed_matrix_holds_its_sizes(L):
+    """A matrix around a buffer of the wrong size, type or sizes is refused before a kernel could read past it."""
+    import torch
+    import speculative_pipeline_decoding_gb300 as spd
+    n = L.spd_q4_packed_bytes(40, 256, 128, 1, 0)
+    ok = torch.zeros(n, dtype=torch.uint8)
+    W = spd.Q4Matrix(ok, 40, 256, 128, torch.bfloat16, False)
+    assert (W.packed is ok, W.rows, W.cols, W.group, W.has_zeros) == (True, 40, 256, 128, False)
+    for a in ((ok[:-1], 40, 256, 128, torch.bfloat16, False), (ok, 49, 256, 128, torch.bfloat16, False), (ok, 40, 256, 128, torch.float32, False),
+              (ok, 40, 256, 128, torch.bfloat16, True), (ok, 40, 256, 96, torch.bfloat16, False), (ok, 0, 256, 128, torch.bfloat16, False),
+              (ok.view(torch.int8), 40, 256, 128, torch.bfloat16, False), (ok, 40 + (1 << 32), 256, 128, torch.bfloat16, False),
+              (torch.zeros(2 * n, dtype=torch.uint8)[::2], 40, 256, 128, torch.bfloat16, False), (ok, 40, 256, 128, torch.float16, False)):
+        with pytest.raises(spd.SpdError):
+            spd.Q4Matrix(*a)
+    with pytest.raises(spd.SpdError):  # on the host
+        spd.q4_gemv([W], [torch.zeros(256)], [torch.zeros(40)])
+    with pytest.raises(AttributeError):
+        W.rows = 80
+
+
+def test_sizes_beyond_32_bits_are_refused(L):
+    import torch
+    import speculative_pipeline_decoding_gb300 as spd
+    assert spd.shared_prefix_attention_workspace_bytes(4, 8, 2, 128, (1 << 32) + 1) == 0
+    assert spd.shared_prefix_attention_workspace_bytes((1 << 32) + 1, 8, 2, 128, 1) == 0
+    W = spd.Q4Matrix(torch.zeros(L.spd_q4_packed_bytes(1, 128, 128, 1, 0), dtype=torch.uint8), 1, 128, 128, torch.bfloat16, False)
+    x, y = torch.zeros(1, 128).expand((1 << 32) + 1, 128), torch.zeros(1, 1).expand((1 << 32) + 1, 1)
+    with pytest.raises(spd.SpdError):
+        spd.q4_gemv([W], [x], [y])
+
+
+def test_a_copied_plan_owns_its_memory(L):
+    import copy
+    import pickle
+    import speculative_pipeline_decoding_gb300 as spd
+    r = spd.Rope(128, 64, theta=5e5)
+    for c in (copy.deepcopy(r), pickle.loads(pickle.dumps(r))):
+        assert (c.head_dim, c.rot_dim) == (128, 64) and ctypes.addressof(c.c) != ctypes.addressof(r.c)
+        assert bytes(c.c) == bytes(r.c) and not any(v == ctypes.addressof(r.c) for v in vars(c).values() if isinstance(v, int))

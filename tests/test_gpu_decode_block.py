@@ -616,3 +616,15 @@ def test_decode_block_captured_and_replayed(spd):
         torch.cuda.synchronize()
         for name in ("y", "kc", "vc", "lens", "pos", "q", "o"):
             assert torch.equal(eager[name], graph[name]), (step, name)
+
+
+def test_a_matrix_read_back_gives_the_same_products(spd):
+    """The packed buffer is all of a matrix: through host memory and into a new object, bit for bit."""
+    g = _g(77)
+    W = spd.q4_pack(*spd.q4_quantize(_rn(g, 100, 384, dtype=BF16), group=64, symmetric=False))
+    x, y, z = _rn(g, 3, 384), torch.empty(3, 100, device="cuda"), torch.empty(3, 100, device="cuda")
+    spd.q4_gemv([W], [x], [y])
+    again = spd.Q4Matrix(W.packed.cpu().cuda(), W.rows, W.cols, W.group, W.scale_dtype, W.has_zeros)
+    del W
+    spd.q4_gemv([again], [x], [z])
+    assert torch.equal(y, z)
