@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Dict, Optional, Sequence, Tuple
 
@@ -667,6 +668,9 @@ def q4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Ten
     return Q4Matrix(packed, rows, cols, group, scales.dtype, zeros is not None)
 
 
+_Q4_GROUPS = [struct.Struct(f"{6 * G}q") for G in range(35)]
+
+
 def q4_gemv(Ws: Sequence[Q4Matrix], xs: Sequence[torch.Tensor], ys: Sequence[torch.Tensor],
             norm_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None) -> None:
     """ys[g][m] = Ws[g] @ (rmsnorm(xs[g][m]) * norm_weight if norm_weight is given else xs[g][m]) for up to 32 vectors m.
@@ -686,18 +690,28 @@ def q4_gemv(Ws: Sequence[Q4Matrix], xs: Sequence[torch.Tensor], ys: Sequence[tor
     M = 1 if nd == 1 else shape[0]
     if dev < 0 or M > 32:
         raise _bad("q4_gemv takes matrices on the GPU and up to 32 vectors")
-    words = []  # the fields of spd_q4_group, 8 bytes each (rows and reserved share one)
+    words, last = [], None  # the fields of spd_q4_group, 8 bytes each (rows and reserved share one)
     for W, x, y in zip(Ws, xs, ys):
+        w, rows = W._packed, W._rows
         if W._kind != kind:
             raise _bad("the matrices of a call share columns, group, scale dtype and zero points")
-        sx, sy, w, rows = x.stride(), y.stride(), W._packed, W._rows
-        if x.dtype is not dt or y.dtype is not dt or x.shape != shape or y.shape != (shape[:-1] + (rows,)):
-            raise _bad(f"xs must be [M, {cols}] and ys [M, rows of the matrix], in one dtype, with one M")
-        if shape[-1] != cols or sx[-1] != 1 or (sy[-1] != 1 and rows > 1):
-            raise _bad(f"x and y rows must be contiguous, x of {cols} columns")
-        if x.get_device() != dev or y.get_device() != dev or w.get_device() != dev:
+        if x is not last:  # the matrices of a call often share their vectors
+            sx = x.stride()
+            if x.dtype is not dt or x.shape != shape or shape[-1] != cols:
+                raise _bad(f"xs must be [M, {cols}], in one dtype, with one M")
+            if sx[-1] != 1:
+                raise _bad("x and y rows must be contiguous")
+            if x.get_device() != dev:
+                raise _bad("tensors must live on one GPU")
+            last, xp, xs_ = x, x.data_ptr(), sx[0] if M > 1 else 0
+        sy, ysh = y.stride(), y.shape
+        if y.dtype is not dt or len(ysh) != nd or ysh[-1] != rows or (nd == 2 and ysh[0] != M):
+            raise _bad("ys must be [M, rows of the matrix], in xs' dtype, with one M")
+        if sy[-1] != 1 and rows > 1:
+            raise _bad("x and y rows must be contiguous")
+        if y.get_device() != dev or w.get_device() != dev:
             raise _bad("tensors must live on one GPU")
-        words += (w.data_ptr(), x.data_ptr(), y.data_ptr(), sx[0] if M > 1 else 0, sy[0] if M > 1 else 0, rows)
+        words += (w.data_ptr(), xp, y.data_ptr(), xs_, sy[0] if M > 1 else 0, rows)
     nw = None
     if norm_weight is not None:
         if (norm_weight.dtype is not torch.float32 or norm_weight.shape != (cols,) or not norm_weight.is_contiguous()
@@ -706,8 +720,7 @@ def q4_gemv(Ws: Sequence[Q4Matrix], xs: Sequence[torch.Tensor], ys: Sequence[tor
         nw = norm_weight.data_ptr()
     if M == 0:
         return
-    arr = (ctypes.c_int64 * len(words))(*words)
-    _call(lib().spd_q4_gemv, dev, (ctypes.addressof(arr), G, M, cols, kind[1], kind[2], kind[3], _DT[dt], nw, eps,
+    _call(lib().spd_q4_gemv, dev, (_Q4_GROUPS[G].pack(*words), G, M, cols, kind[1], kind[2], kind[3], _DT[dt], nw, eps,
                                    _stream_of(dev, stream)))
 
 
