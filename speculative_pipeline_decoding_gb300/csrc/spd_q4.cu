@@ -18,8 +18,10 @@
 // off; both are exact for zeros up to 240.  Columns beyond `cols` and rows beyond `rows` hold code = zero and scale 0.
 //
 // Measured (graph of calls on different weights, against the bytes at the copy bandwidth): 151936 x 2560, one fp32 vector
-// 46 us for 201 MB (64 %); 2 x 12288 x 4096, 8 bf16 vectors, groups of 64 with zeros 19 us for 56 MB (42 %); Q, K and V of
-// 6144 x 4096 for one vector 8.7 us for 13 MB, of which some 6 us are launch, splitting the vector and joining.
+// 47 us for 201 MB (63 %); 2 x 12288 x 4096, 8 bf16 vectors, groups of 64 with zeros 18 us for 56 MB (45 %); Q, K and V of
+// 6144 x 4096 for one vector 8.5 us for 13 MB, of which some 6 us are launch, splitting the vector and joining; 4096 x 12288,
+// 16 vectors: bf16 16 us, fp32 37.
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -133,6 +135,7 @@ struct Params {
   int G, M, cols, nkb, tiles;
   int rec, s_f32, has_z, x_f32;
   int terms, mb;     // bf16 terms of a vector, vectors of a block
+  int cluster;       // blocks that share the columns of a run of tiles
   int chunk, batch;  // column blocks of the vectors in shared memory at a time; tiles between two meetings of the warps
   const float* nw;
   int nvec;          // nw starts on 16 bytes
@@ -166,45 +169,73 @@ __device__ __forceinline__ void split8(float* v, int terms, uint4* dst, int step
   float f = 0.f;  // 0 if all are finite, else NaN
 #pragma unroll
   for (int j = 0; j < 8; ++j) f = fmaf(v[j], 0.f, f);
-  for (int e = 0; e < terms; ++e, dst += step) {
-    uint32_t o[4];
-    if (f == 0.f) {
-      if (e == 1 && terms == 2) {
+  if (f == 0.f) {
+    auto upper = [&](uint4* d) {
+      uint32_t o[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-          o[j] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-      } else {
+      for (int j = 0; j < 4; ++j) o[j] = __byte_perm(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]), 0x7632);
+      *d = make_uint4(o[0], o[1], o[2], o[3]);
+    };
+    auto rest = [&]() {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = __byte_perm(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]), 0x7632);
+      for (int j = 0; j < 8; ++j) v[j] -= __uint_as_float(__float_as_uint(v[j]) & 0xffff0000u);
+    };
+    upper(dst);
+    if (terms == 1) return;
+    rest();
+    if (terms == 2) {
+      uint32_t o[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] -= __uint_as_float(__float_as_uint(v[j]) & 0xffff0000u);
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        o[j] = *reinterpret_cast<const uint32_t*>(&h);
       }
-    } else {
-      // infinities and NaN stay what they are in the first term; a NaN keeps a bit in its upper half
-      uint32_t h[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        h[j] = (__float_as_uint(v[j]) | (v[j] != v[j] ? 0x400000u : 0u)) & 0xffff0000u;
-        v[j] = fabsf(v[j]) < INFINITY ? v[j] - __uint_as_float(h[j]) : 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = h[2 * j] >> 16 | h[2 * j + 1];
+      dst[step] = make_uint4(o[0], o[1], o[2], o[3]);
+      return;
     }
-    *dst = make_uint4(o[0], o[1], o[2], o[3]);
+    upper(dst + step);
+    rest();
+    upper(dst + 2 * step);
+    return;
+  }
+  // infinities and NaN stay what they are in the first term; a NaN keeps a bit in its upper half
+  for (int e = 0; e < terms; ++e, dst += step) {
+    uint32_t h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      h[j] = (__float_as_uint(v[j]) | (v[j] != v[j] ? 0x400000u : 0u)) & 0xffff0000u;
+      v[j] = fabsf(v[j]) < INFINITY ? v[j] - __uint_as_float(h[j]) : 0.f;
+    }
+    *dst = make_uint4(h[0] >> 16 | h[1], h[2] >> 16 | h[3], h[4] >> 16 | h[5], h[6] >> 16 | h[7]);
   }
 }
-// Bytes of dynamic shared memory: vectors of a chunk and 64 zero bytes, parts of the warps, sums over the chunks so far.
+// Bytes of dynamic shared memory: vectors of a chunk, parts of the warps, sums over the chunks so far or of
+// a block's share of the columns.
 struct Smem {
   uint32_t part, sums, total;
 };
-__host__ __device__ inline Smem smem_of(int chunk, int nkb, int ncol, int nt, int batch, int mb) {
+__host__ __device__ inline Smem smem_of(const Params& p, int nt) {
   Smem s;
-  s.part = (uint32_t)chunk * 4 * ncol * 64 + 64;
-  s.sums = s.part + (uint32_t)(batch + kWarps - 1) * 16 * (nt * 8 + 1) * 4;
-  s.total = s.sums + (chunk < nkb ? (uint32_t)16 * batch * mb * 4 : 0);
+  s.part = (uint32_t)p.chunk * 4 * p.mb * p.terms * 64;
+  s.sums = s.part + (uint32_t)(p.batch + kWarps - 1) * 16 * (nt * 8 + 1) * 4;
+  s.total = s.sums + (p.cluster > 1 || p.chunk < p.nkb ? (uint32_t)16 * p.batch * p.mb * 4 : 0);
   return s;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(const float* p, int rank) {  // the same variable of another block of the cluster
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ uint4 ld16(const unsigned char* p) {  // read once: not kept in L1
@@ -234,11 +265,13 @@ template <int NG> struct Record {
   uint32_t s[2 * NG], z[NG];  // fp32 scales, or bf16 ones in the first half; zeros
 };
 
-// A block owns a run of tiles and takes them in batches.  The records of a batch are dealt to its 8 warps in equal runs,
+// A block, or a cluster of two or four that share the columns, owns a run of tiles and takes them in batches.  The records of a
+// batch are dealt to a block's 16 warps in equal runs,
 // whatever tiles they fall into: a warp reads its run as one stream, kAhead records ahead in registers, and leaves the sum of
 // each tile it touched in shared memory, as part warp + tile.  The warps meet once a batch, to add the parts up in their
 // order.  The vectors are split into terms once per block, as [column block][word][operand column][t] of 16 bytes (two mma
-// steps of a lane); where they do not fit at once the columns are taken in chunks, sums over the chunks in shared memory.
+// steps of a lane); where they do not fit at once the columns are taken in chunks, sums over the chunks in shared memory.  The
+// blocks of a cluster read one another's sums there, in the blocks' order.
 // The limit besides memory is the instruction rate: about 11 instructions a word of 8 codes, 88 of some 130 a record.
 template <int NT, int GW>  // operand tiles; 32-column words of a group (1, 2, 4)
 __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant__ Params p) {
@@ -248,22 +281,18 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
   constexpr int kAhead = NT == 1 ? 4 : NT == 2 ? (NG < 4 ? 4 : 3) : 2;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g4 = lane >> 2, t4 = lane & 3;
   const int m0 = blockIdx.y * p.mb, mb = min(p.mb, p.M - m0), ncol = mb * p.terms;
-  const int nc = gridDim.x, cid = blockIdx.x;
+  // a cluster takes a run of tiles, a block of it a share of their columns
+  const int C = p.cluster, cr = C > 1 ? (int)cluster_rank() : 0, nc = gridDim.x / C, cid = blockIdx.x / C;
+  const int kb0 = cr * p.nkb / C, kb1 = (cr + 1) * p.nkb / C;
   const int first = cid * (p.tiles / nc) + min(cid, p.tiles % nc), last = first + p.tiles / nc + (cid < p.tiles % nc);
-  const Smem L = smem_of(p.chunk, p.nkb, p.mb * p.terms, NT, p.batch, p.mb);
+  const Smem L = smem_of(p, NT);
   uint4* xs = reinterpret_cast<uint4*>(smem);
   float* part = reinterpret_cast<float*>(smem + L.part);  // [batch + 7][16][NT * 8 + 1]
   float* sums = reinterpret_cast<float*>(smem + L.sums);  // [mb][16 * batch]
   __shared__ float s_ss[kWarps][kMaxM], s_sum[kMaxM];
-  if (tid < 4) reinterpret_cast<uint4*>(smem + L.part - 64)[tid] = make_uint4(0, 0, 0, 0);
-  // this lane's column of each operand tile; columns that do not exist read the zero bytes, at a step of 0
-  uint32_t x0[NT], xstep[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const bool in = n * 8 + g4 < ncol;
-    x0[n] = in ? ((n * 8 + g4) * 4 + t4) * 16 : L.part - 64 + t4 * 16;
-    xstep[n] = in ? ncol * 64 : 0;
-  }
+  // This lane's column of the first operand tile; the others' lie 512 bytes apart.  Columns from ncol on do not exist: they read
+  // what follows (other columns, or the parts), and their sums are not used.
+  const uint32_t x0 = (g4 * 4 + t4) * 16, xstep = ncol * 64;
   uint32_t magic;
   asm volatile("mov.b32 %0, 0x41804180;" : "=r"(magic));
   const uint32_t soff = 1024 + g4 * (2 * NG) * (p.s_f32 ? 4 : 2), zoff = 1024 + 16 * NG * (p.s_f32 ? 4 : 2) + g4 * (2 * NG) * 2;
@@ -273,6 +302,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
     if (p.s_f32) ld_words<2 * NG>(src + soff, r.s);
     else ld_words<NG>(src + soff, r.s);
     if (p.has_z) ld_words<NG>(src + zoff, r.z);
+  };
+  auto finish = [&](const Group& G, int m, int row, float y, float ss) {
+    if (p.nw) y *= rsqrtf(ss / p.cols + p.eps);
+    const long long at = (long long)(m0 + m) * G.ys + row;
+    if (p.x_f32) static_cast<float*>(G.y)[at] = y;
+    else static_cast<__nv_bfloat16*>(G.y)[at] = __float2bfloat16_rn(y);
   };
   pdl_wait();
   pdl_trigger();
@@ -285,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
     t1 = min(last, t0 + p.batch);
     if (gi + 1 < p.G) t1 = min(t1, p.g[gi + 1].tile0);
     const int nrow = 16 * (t1 - t0);
-    for (int kb_lo = 0; kb_lo < p.nkb; kb_lo += p.chunk) {
-      const int nk = min(p.chunk, p.nkb - kb_lo);
+    for (int kb_lo = kb0; kb_lo < kb1; kb_lo += p.chunk) {
+      const int nk = min(p.chunk, kb1 - kb_lo);
       const int nrec = (t1 - t0) * nk, r0 = warp * nrec / kWarps, r1 = (warp + 1) * nrec / kWarps;
       int u = r0 / nk, kb = r0 - u * nk;
       const unsigned char* src = G.w + ((size_t)(t0 - G.tile0 + u) * p.nkb + kb_lo + kb) * p.rec;
@@ -325,11 +360,15 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
           asm volatile("cp.async.commit_group;\n cp.async.wait_group 0;" ::: "memory");
         } else {
           constexpr int kU = 2;
+          const float inv = 1.f / segs;  // of (q + 1/2) / segs, which is 1/2048 or more off a whole number and below 2048
           for (int q0 = warp; q0 < nseg; q0 += kWarps * kU) {
             float v[kU][8], nw[kU][8];
+            int mk[kU], ik[kU];
 #pragma unroll
             for (int k = 0; k < kU; ++k) {
-              const int q = q0 + k * kWarps, m = q / segs, i = (q - m * segs) * 32 + lane, c = c0 + i * 8;
+              const int q = q0 + k * kWarps, m = (int)((q + 0.5f) * inv), i = (q - m * segs) * 32 + lane, c = c0 + i * 8;
+              mk[k] = m;
+              ik[k] = i;
 #pragma unroll
               for (int j = 0; j < 8; ++j) v[k][j] = 0.f;
               if (q >= nseg || i >= per || c >= p.cols) continue;
@@ -365,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
             }
 #pragma unroll
             for (int k = 0; k < kU; ++k) {
-              const int q = q0 + k * kWarps, m = q / segs, i = (q - m * segs) * 32 + lane, c = c0 + i * 8;
-              if (q >= nseg) continue;  // the whole warp
+              const int m = mk[k], i = ik[k], c = c0 + i * 8;
+              if (q0 + k * kWarps >= nseg) continue;  // the whole warp
               if (p.nw) {
                 float ss = 0.f;
                 if (i < per && c < p.cols) {
@@ -387,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
         }
         __syncthreads();
         if (p.nw && tid < mb) {
-          float ss = kb_lo ? s_sum[tid] : 0.f;
+          float ss = kb_lo > kb0 ? s_sum[tid] : 0.f;
           for (int w = 0; w < kWarps; ++w) ss += s_ss[w][tid];
           s_sum[tid] = ss;  // read behind the barrier of the parts
         }
@@ -421,9 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
           if (at + j >= r1) break;
           const Record<NG>& r = rec[j];
           const uint32_t w0[4] = {r.a0.x, r.a0.y, r.a0.z, r.a0.w}, w1[4] = {r.a1.x, r.a1.y, r.a1.z, r.a1.w};
-          uint32_t xk[NT];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) xk[n] = x0[n] + (uint32_t)kb * 4 * xstep[n];
+          uint32_t xk = x0 + (uint32_t)kb * 4 * xstep;
           uint32_t z0 = 0xc1c0c1c0u, z1 = z0;  // -24, -24
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
@@ -434,10 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
             }
             uint4 b[NT];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              b[n] = *reinterpret_cast<const uint4*>(smem + xk[n]);
-              xk[n] += xstep[n];
-            }
+            for (int n = 0; n < NT; ++n) b[n] = *reinterpret_cast<const uint4*>(smem + xk + n * 512);
+            xk += xstep;
             const uint32_t zz[4] = {z0, z1, z0, z1};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -486,36 +521,51 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
       }
       if (r0 == r1) flush();  // an empty run between two others of a tile
       __syncthreads();
-      // A thread finishes an output: row r of the batch, which is row r % 16 of tile r / 16, for vector m.  Its parts are
-      // those of the warps whose runs touch the tile; the small terms are added first.
-      const bool done = kb_lo + nk == p.nkb;
-      for (int o = tid; o < nrow * mb; o += kThreads) {
-        const int m = o / nrow, r = o - m * nrow, row = (t0 - G.tile0) * 16 + r, tl = r >> 4;
-        if (row >= G.rows) continue;
+      // Warps take tiles, or shares of a tile's vectors where there are fewer tiles; half a warp the 16 rows for a vector.  The
+      // parts of a tile are those of the warps whose runs touch it; the small terms are added first.
+      const bool done = kb_lo + nk == kb1;
+      const int nt = t1 - t0, ws = nt < kWarps ? kWarps / nt : 1;
+      for (int tl = nt < kWarps ? warp % nt : warp; tl < nt && warp < (nt < kWarps ? ws * nt : kWarps); tl += kWarps) {
         const int wa = ((tl * nk + 1) * kWarps - 1) / nrec, np = ((tl + 1) * nk * kWarps - 1) / nrec - wa + 1;
-        const float* q = part + ((wa + tl) * 16 + (r & 15)) * PC + m * p.terms;
-        float y = kb_lo ? sums[o] : 0.f;
-        for (int w = 0; w < np; w += 4) {
-          float v[4];
+        const int r = tl * 16 + (lane & 15), row = (t0 - G.tile0) * 16 + r;
+        for (int m = (nt < kWarps ? warp / nt : 0) * 2 + (lane >> 4); m < mb; m += 2 * ws) {
+          const float* q = part + ((wa + tl) * 16 + (r & 15)) * PC + m * p.terms;
+          const int o = m * nrow + r;
+          float y = kb_lo > kb0 ? sums[o] : 0.f;
+          for (int w = 0; w < np; w += 4, q += 4 * 16 * PC) {
+            float v[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            v[k] = 0.f;
-            if (w + k < np)
-              for (int e = p.terms - 1; e >= 0; --e) v[k] += q[(w + k) * 16 * PC + e];
+            for (int k = 0; k < 4; ++k) {
+              v[k] = 0.f;
+              if (w + k < np) {
+                const float* qk = q + k * 16 * PC;
+                if (p.terms == 3) v[k] = qk[2];
+                if (p.terms > 1) v[k] += qk[1];
+                v[k] += qk[0];
+              }
+            }
+            y += v[0];
+            y += v[1];
+            y += v[2];
+            y += v[3];
           }
-          y += v[0];
-          y += v[1];
-          y += v[2];
-          y += v[3];
+          if (!done || C > 1) sums[o] = y;
+          else if (row < G.rows) finish(G, m, row, y, p.nw ? s_sum[m] : 0.f);
         }
-        if (!done) {
-          sums[o] = y;
-          continue;
+      }
+      if (done && C > 1) {  // the blocks' shares, each block a part of the outputs; the order is the blocks'
+        cluster_sync();
+        for (int o = cr * kThreads + tid; o < nrow * mb; o += C * kThreads) {
+          const int m = o / nrow, r = o - m * nrow, row = (t0 - G.tile0) * 16 + r;
+          if (row >= G.rows) continue;
+          float y = 0.f, ss = 0.f;
+          for (int c = 0; c < C; ++c) {
+            y += ld_cluster(sums + o, c);
+            if (p.nw) ss += ld_cluster(s_sum + m, c);
+          }
+          finish(G, m, row, y, ss);
         }
-        if (p.nw) y *= rsqrtf(s_sum[m] / p.cols + p.eps);
-        const long long at = (long long)(m0 + m) * G.ys + row;
-        if (p.x_f32) static_cast<float*>(G.y)[at] = y;
-        else static_cast<__nv_bfloat16*>(G.y)[at] = __float2bfloat16_rn(y);
+        cluster_sync();  // the shares are read
       }
       if (!done || t1 < last) __syncthreads();  // the parts and the vectors are read
     }
@@ -543,11 +593,14 @@ cudaError_t launch(const Params& p, dim3 grid, size_t smem, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, gemv_kernel<NT, GW>, p);
 }
 template <int NT>
@@ -555,23 +608,77 @@ cudaError_t launch_gw(const Params& p, int group, dim3 grid, size_t smem, cudaSt
   return group == 128 ? launch<NT, 4>(p, grid, smem, s) : group == 64 ? launch<NT, 2>(p, grid, smem, s) : launch<NT, 1>(p, grid, smem, s);
 }
 
-// How the work is cut, for one block an SM: sets mb, chunk and batch; returns the operand tiles of a warp.
+inline int min_i(int a, int b) { return a < b ? a : b; }
+
+// Clusters of C blocks, a block an SM, that run at once.
+int clusters_of(int C, int sms) {
+  if (C == 1) return sms;
+  static std::atomic<int> have[64][5];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = 64;
+  if (dev < 64 && (n = have[dev][C].load(std::memory_order_relaxed)) > 0) return n;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)C);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 128 * 1024;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(gemv_kernel<1, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, gemv_kernel<1, 4>, &cfg) != cudaSuccess || n < 1)
+    n = 1;
+  if (dev < 64) have[dev][C].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// How a cluster of C blocks, each with a share of the columns, takes its tiles.  Sets cluster, chunk and batch; returns an
+// estimate of the time in ns, beside what does not depend on C.
+//   chunk: the column blocks of a share, if they leave room for 8 tiles in 224 KB, else even shares of them.
+//   batch: even shares of the cluster's tiles, as far as the rest and 96 KB of parts hold.
+// The estimate's terms were measured a block: splitting a column block of a vector 8 ns a term, a record 20 ns and 20 more an
+// operand tile, a meeting of a cluster 1 us and half a ns an output.
+double cut(Params* p, int nt, int C, int sms) {
+  p->cluster = C;
+  const int nc = min_i(p->tiles, clusters_of(C, sms)), own = (p->tiles + nc - 1) / nc, share = (p->nkb + C - 1) / C;
+  const int tile = 16 * (nt * 8 + 1) * 4, room = 224 * 1024;
+  static_assert(96 * 1024 / (16 * (6 * 8 + 1) * 4) >= kWarps, "a batch holds a tile at least");
+  const int most = 96 * 1024 / tile - kWarps + 1;
+  const long long left = (long long)room - (long long)share * p->mb * p->terms * 256 - (long long)(kWarps - 1) * tile;
+  const long long fit = left / (tile + 64 * p->mb);
+  const bool whole = fit >= min_i(own, 8);
+  const int n = (own + min_i(own, whole && fit < most ? (int)fit : most) - 1) / min_i(own, whole && fit < most ? (int)fit : most);
+  p->batch = (own + n - 1) / n;
+  p->chunk = share;
+  for (int k = 2; p->chunk > 1 && smem_of(*p, nt).total > room; ++k) p->chunk = (share + k - 1) / k;
+  const double split = 8.0 * p->terms * p->mb * share * (p->chunk < share ? n : 1), records = (20.0 + 20.0 * nt) * own * share;
+  return split + records + (C > 1 ? 1000.0 * (n + p->G - 1) + 0.5 * 16 * own * p->mb : 0.0);
+}
+
+// Sets mb, cluster, chunk and batch; returns the operand tiles of a warp.
 //   mb: at most 48 operand columns (6 tiles of accumulators), in even shares.  More vectors in a pass read the weights less
 //       often; 6 tiles are what 128 registers hold beside the records ahead.
-//   batch: the tiles of a block, as far as 96 KB of parts hold.
-//   chunk: all columns if they fit the rest of 224 KB, else even shares of them.
+//   cluster: 1, or 2 or 4 where that looks a tenth faster, which it does for wide vectors and few rows.  By blocks of their own /
+//       clusters of 4: 4096 x 12288, 16 fp32 vectors 72 / 37 us, bf16 23 / 16; 2086 x 5632, 5 fp32 11.2 / 9.3; but 24576 x 4096, 8
+//       bf16 18 / 23 (its sums cost more than its vectors), 6144 x 4096, one fp32 8.5 / 11.3.  Clusters of 8 lose a fifth of the
+//       SMs, which come in groups that are no multiple of 8.
 int plan(Params* p, int sms) {
   const int parts = (p->M * p->terms + 47) / 48;
   p->mb = (p->M + parts - 1) / parts;
   int nt = (p->mb * p->terms + 7) / 8;
   if (nt > 4) nt = 6;
-  static_assert(96 * 1024 / (16 * (6 * 8 + 1) * 4) >= kWarps, "a batch holds a tile at least");
-  const int own = (p->tiles + sms - 1) / sms, most = 96 * 1024 / (16 * (nt * 8 + 1) * 4) - kWarps + 1;
-  p->batch = own < most ? own : most;
-  for (int n = 1;; ++n) {
-    p->chunk = (p->nkb + n - 1) / n;
-    if (smem_of(p->chunk, p->nkb, p->mb * p->terms, nt, p->batch, p->mb).total <= 224 * 1024) return nt;
+  const double alone = cut(p, nt, 1, sms);
+  int best = 1;
+  double t = 0.9 * alone;
+  for (int C = 2; C <= 4 && C <= p->nkb; C *= 2) {
+    const double u = cut(p, nt, C, sms);
+    if (u < t) best = C, t = u;
   }
+  if (p->cluster != best) cut(p, nt, best, sms);
+  return nt;
 }
 
 bool sizes_ok(int rows, int cols, int group, int scale_dtype) {
@@ -665,9 +772,10 @@ extern "C" int spd_q4_gemv(const spd_q4_group* groups, int32_t G, int32_t M, int
   p.s_f32 = scale_dtype == SPD_DTYPE_F32; p.has_z = has_zeros != 0; p.x_f32 = x_dtype == SPD_DTYPE_F32;
   p.nw = nw; p.eps = eps; p.nvec = q4::aligned(nw, 16);
   p.terms = p.x_f32 ? 3 : nw ? 2 : 1;
-  const int sms = num_sms(), nt = q4::plan(&p, sms);
-  const size_t smem = q4::smem_of(p.chunk, p.nkb, p.mb * p.terms, nt, p.batch, p.mb).total;
-  const dim3 grid((unsigned)(p.tiles < sms ? p.tiles : sms), (unsigned)((M + p.mb - 1) / p.mb));
+  const int nt = q4::plan(&p, num_sms());
+  const size_t smem = q4::smem_of(p, nt).total;
+  const int nc = q4::min_i(p.tiles, q4::clusters_of(p.cluster, num_sms()));
+  const dim3 grid((unsigned)(nc * p.cluster), (unsigned)((M + p.mb - 1) / p.mb));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(cuda_stream);
   cudaGetLastError();
   cudaError_t e;

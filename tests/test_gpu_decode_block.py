@@ -628,3 +628,16 @@ def test_a_matrix_read_back_gives_the_same_products(spd):
     del W
     spd.q4_gemv([again], [x], [z])
     assert torch.equal(y, z)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shapes,cols,group,scale_dtype,zeros,M,norm", [
+    ((1000, 33), 12288, 128, BF16, False, 16, True),    # two matrices, one of a few tiles
+    ((700,), 5664, 32, F32, True, 11, False),           # columns that end inside a block of 128 and are no multiple of four blocks
+    ((20,), 640, 64, BF16, True, 32, True),             # fewer columns than threads, fewer tiles than clusters
+    ((4100, 10), 4096, 64, BF16, True, 32, False),      # several batches of tiles
+    ((100, 1, 300), 8192, 128, F32, False, 7, True),
+    ((2400,), 32768, 128, BF16, False, 32, True),       # the widest, in several passes of vectors
+])
+def test_q4_gemv_columns_shared_by_a_cluster(spd, dtype, shapes, cols, group, scale_dtype, zeros, M, norm):
+    _check_gemv(spd, shapes, cols, group, scale_dtype, zeros, M, dtype, norm, spread=True)
