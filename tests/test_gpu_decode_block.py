@@ -641,3 +641,69 @@ def test_a_matrix_read_back_gives_the_same_products(spd):
 ])
 def test_q4_gemv_columns_shared_by_a_cluster(spd, dtype, shapes, cols, group, scale_dtype, zeros, M, norm):
     _check_gemv(spd, shapes, cols, group, scale_dtype, zeros, M, dtype, norm, spread=True)
+
+
+def test_calls_from_threads_on_streams_of_their_own(spd):
+    """Four threads, each with its stream, its block and its workspace, beside one another: what one of them alone gives."""
+    import threading
+    torch.cuda.synchronize()
+    states = [_block_state(spd, BF16, B=32, P=4000, cap=40) for _ in range(5)]
+    wide = [(_rn(_g(5), 9, 8192), torch.empty(9, 70, device="cuda")) for _ in range(5)]
+    W = spd.q4_pack(*spd.q4_quantize(_rn(_g(6), 70, 8192, std=0.05)))
+    assert spd.shared_prefix_attention_workspace_bytes(32, 8, 2, 128, 4000) > 16  # the tensor cores' path
+    torch.cuda.synchronize()
+    failed = []
+
+    def run(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(4):
+                    _block(spd, states[i])
+                    spd.q4_gemv([W], [wide[i][0]], [wide[i][1]])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001 - reported below, in the test's own thread
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    run(4)
+    assert not failed
+    for i in range(4):
+        for name in ("y", "o", "kc", "vc", "lens"):
+            assert torch.equal(states[i][name], states[4][name]), name
+        assert torch.equal(wide[i][1], wide[4][1])
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    """Nothing is set up at a first call that a capture forbids."""
+    import subprocess
+    import sys
+    code = """
+import torch, speculative_pipeline_decoding_gb300 as spd
+dev = dict(device="cuda")
+W = spd.Q4Matrix(torch.zeros(spd.lib().spd_q4_packed_bytes(64, 8192, 128, 1, 0), dtype=torch.uint8, **dev), 64, 8192, 128, torch.bfloat16, False)
+x, y = torch.ones(9, 8192, **dev), torch.full((9, 64), 7.0, **dev)
+B, P = 64, 4000
+q = torch.ones(B, 4, 128, **dev)
+pk = torch.ones(4, P, 128, dtype=torch.bfloat16, **dev)
+kc = torch.ones(B, 4, 16, 128, dtype=torch.bfloat16, **dev)
+lens = torch.full((B,), 5, dtype=torch.int32, **dev)
+ws = torch.empty(spd.shared_prefix_attention_workspace_bytes(B, 4, 4, 128, P), dtype=torch.uint8, **dev)
+o, rope, small = torch.zeros_like(q), spd.Rope(128), torch.zeros(1, 4, 128, **dev)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    spd.rope_append(rope, q, q, lens, k=q, v=q, k_cache=kc, v_cache=kc.clone(), slot=lens, seq=torch.arange(B, dtype=torch.int32, **dev))
+    spd.q4_gemv([W], [x], [y])
+    spd.shared_prefix_attention(q, pk, pk, P, kc, kc, lens, o, ws)
+    spd.shared_prefix_attention(q[:1], pk, pk, 3, None, None, None, small, ws)
+g.replay()
+torch.cuda.synchronize()
+assert not y.any() and (o - 1).abs().max() < 1e-5 and (small - 1).abs().max() < 1e-5
+"""
+    p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-2000:]
