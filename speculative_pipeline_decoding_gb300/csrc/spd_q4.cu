@@ -20,7 +20,7 @@
 // Measured (graph of calls on different weights, against the bytes at the copy bandwidth): 151936 x 2560, one fp32 vector
 // 47 us for 201 MB (63 %); 2 x 12288 x 4096, 8 bf16 vectors, groups of 64 with zeros 18 us for 56 MB (45 %); Q, K and V of
 // 6144 x 4096 for one vector 8.5 us for 13 MB, of which some 6 us are launch, splitting the vector and joining; 4096 x 12288,
-// 16 vectors: bf16 16 us, fp32 37.
+// 16 vectors: bf16 16 us, fp32 30.
 #include <atomic>
 #include <cmath>
 #include <cstdio>
@@ -267,7 +267,7 @@ template <int NG> struct Record {
 
 // A block, or a cluster of two or four that share the columns, owns a run of tiles and takes them in batches.  The records of a
 // batch are dealt to a block's 16 warps in equal runs,
-// whatever tiles they fall into: a warp reads its run as one stream, kAhead records ahead in registers, and leaves the sum of
+// whatever tiles they fall into: a warp reads its run as one stream, one to four records ahead in registers, and leaves the sum of
 // each tile it touched in shared memory, as part warp + tile.  The warps meet once a batch, to add the parts up in their
 // order.  The vectors are split into terms once per block, as [column block][word][operand column][t] of 16 bytes (two mma
 // steps of a lane); where they do not fit at once the columns are taken in chunks, sums over the chunks in shared memory.  The
@@ -278,7 +278,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int NG = 4 / GW, PC = NT * 8 + 1;
   constexpr int kChains = NT == 2 ? 2 : 1;
-  constexpr int kAhead = NT == 1 ? 4 : NT == 2 ? (NG < 4 ? 4 : 3) : 2;
+  // as many as 128 registers hold without a spill, which would go to memory (the L1 is shared memory here): one more cost
+  // 64 -> 74 us at 151936 x 2560, groups of 32, one vector, and 62 -> 77 at 32000 x 2048, 32 fp32 vectors
+  constexpr int kAhead = NT == 1 ? (NG < 4 ? 4 : 3) : NT == 2 ? (NG < 4 ? 4 : 2) : NT == 3 || (NT == 4 && NG < 4) ? 2 : 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g4 = lane >> 2, t4 = lane & 3;
   const int m0 = blockIdx.y * p.mb, mb = min(p.mb, p.M - m0), ncol = mb * p.terms;
   // a cluster takes a run of tiles, a block of it a share of their columns
@@ -662,7 +664,7 @@ double cut(Params* p, int nt, int C, int sms) {
 //   mb: at most 48 operand columns (6 tiles of accumulators), in even shares.  More vectors in a pass read the weights less
 //       often; 6 tiles are what 128 registers hold beside the records ahead.
 //   cluster: 1, or 2 or 4 where that looks a tenth faster, which it does for wide vectors and few rows.  By blocks of their own /
-//       clusters of 4: 4096 x 12288, 16 fp32 vectors 72 / 37 us, bf16 23 / 16; 2086 x 5632, 5 fp32 11.2 / 9.3; but 24576 x 4096, 8
+//       clusters of 4: 4096 x 12288, 16 fp32 vectors 72 / 37 us, bf16 23 / 16; 2086 x 5632, 5 fp32 11.2 / 8.8; but 24576 x 4096, 8
 //       bf16 18 / 23 (its sums cost more than its vectors), 6144 x 4096, one fp32 8.5 / 11.3.  Clusters of 8 lose a fifth of the
 //       SMs, which come in groups that are no multiple of 8.
 int plan(Params* p, int sms) {
