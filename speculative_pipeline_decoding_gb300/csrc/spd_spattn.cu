@@ -14,8 +14,8 @@
 // whatever the buffer holds.  bf16 queries: two tiles a block alternate, one in the tensor core while the other's softmax
 // runs.  fp32 queries: one tile, Q and P as three bf16 terms (x = t0 + t1 + t2 to 24 bits), small terms first.  bf16
 // queries' probabilities are rounded to bf16 once, which adds to the output what its own rounding does (2^-9 of the rms).
-// The work, (row tiles) x (chunks), is cut into equal runs, one per SM; a run that crosses from one tile to the next leaves
-// a part for each.  A chunk (64 KB at hd 128) is 2 x 2.1 M MACs a tile, 1024 cycles of tensor core, and 2790 cycles of an
+// The work, (row tiles) x (chunks), is cut into runs, one per SM, that end with their tiles where that leaves few SMs idle; a
+// run that crosses from one tile to the next leaves a part for each.  A chunk (64 KB at hd 128) is 2 x 2.1 M MACs a tile, 1024 cycles of tensor core, and 2790 cycles of an
 // SM's share of the memory: that bounds up to about 256 rows a kv head, softmax and tensor core beyond (measured a chunk of
 // two tiles: 850 cycles of exponentials, 400 of maxima, 2 x 1024 of MMAs).  Alone, 64 x 4 rows a kv head x 32768 keys take
 // 30 us (134 MB: 4.5 TB/s, 1.1 PFLOP/s).
@@ -25,8 +25,8 @@
 // at a time, on mma.sync m16n8k16: S^T = K Q^T (16 keys x 8 heads), then O^T += V^T P^T (16 head elements x 8 heads).  K and
 // V come by tensor copies with the 128-byte swizzle, from which ldmatrix takes both operands without bank conflicts.
 //
-// join kernel: the parts of a row, weighted and added.  256 sequences of at most 512 own keys over 8192 shared ones: 85 us in
-// all for 306 MB (45 us at the copy bandwidth): beside one another the prefix kernel takes 57 us and the parts kernel 72
+// join kernel: the parts of a row, weighted and added.  256 sequences of at most 512 own keys over 8192 shared ones: 75 us in
+// all for 306 MB (45 us at the copy bandwidth): beside one another the prefix kernel takes 47 us and the parts kernel 61
 // (alone 30 and 50), then the join 8.
 //
 // rows kernel: all keys of a sequence in one kernel, where the prefix is too short for the tensor cores to gain anything.
@@ -1086,17 +1086,31 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Par
 // Prefix keys through the tensor cores, or read by the rows kernel of every sequence: the tensor cores' part costs some 8 us
 // before it gains anything.  Bytes that all sequences together would read: at 17 MB (32 x 128 keys, 8 kv heads) 7.8 us
 // directly and 11.0 through the tensor cores, at 34 MB (4 x 2048) 11.5 and 12.3, at 67 MB (16 x 1024) 15.7 and 11.8, at 155 MB
-// (17 x 1111, 16 kv heads, fp32 queries) 32 and 25.
-bool prefix_pays(int B, int hkv, int hd, int P) { return (long long)B * hkv * P * hd * 4 > (48LL << 20); }
+// (17 x 1111, 16 kv heads, fp32 queries) 32 and 25.  Few sequences and heads read a long prefix with too few warps (32 a head
+// at most): one sequence, one kv head, bf16, 6000 keys 14.7 directly and 15.2, 9000 keys 19.2 and 15.8, 16000 29 and 18.
+bool prefix_pays(int B, int hkv, int hd, int P) { return (long long)B * hkv * P * hd * 4 > (48LL << 20) || P > 8192; }
 
-// Units, runs and chunks of the prefix kernel; `ns` row tiles a unit.
+// Units, runs and chunks of the prefix kernel; `ns` row tiles a unit.  Runs that end with their unit are best, as many of a unit
+// as the SMs hold: a run across two units loads queries and writes sums twice, and stalls between.  256 x 8192 keys, 8 kv heads,
+// bf16: 32 units in 128 runs of 16 chunks 74 us, in 152 runs of 13 or 14 across units 85; 256 x 6000, 4 kv heads, fp32: 56 units
+// in 112 runs of 24 93 us, 152 of 17 or 18 98.  Where that leaves more SMs idle, equal runs over all units.
+// A run has c chunks at least, with 8 c^2 >= the chunks of a unit: the more runs, the more parts the join reads one after the
+// other, and the fewer SMs are left to the own keys beside.  One sequence, one kv head, bf16, 16000 keys: 125 runs of one chunk
+// 28 us, 32 of four 18; 17 x 1111 keys, 16 kv heads, fp32: 144 runs of one 24 us, 80 of one or two 18.
 void prefix_geometry(int rows, int hkv, int P, int ns, int sms, Params* p) {
   p->units_per_kv = (rows + ns * kTile - 1) / (ns * kTile);
   p->units = hkv * p->units_per_kv;
   p->tiles = rows <= kTile ? 1 : ns;  // tiles that a unit can have
   p->nch = (P + kTile - 1) / kTile;
   const long long total = (long long)p->units * p->nch;
-  p->n_cta = (int)(total < sms ? total : sms);
+  const int most = sms / p->units, even = (int)((total + sms - 1) / sms);
+  int c = most > 0 ? (p->nch + most - 1) / most : p->nch;
+  if (most > 0 && c <= even + even / 4 + 3) {
+    while (8LL * c * c < p->nch) ++c;
+    p->n_cta = p->units * ((p->nch + c - 1) / c);
+  } else {
+    p->n_cta = (int)(total < sms ? total : sms);
+  }
 }
 size_t part_rows(const Params& p, int ns) { return ((size_t)p.n_cta + p.units) * ns * kTile; }
 // Runs of a sequence's own keys: 4096 in all where the batch is smaller, 16 of a sequence at most.
