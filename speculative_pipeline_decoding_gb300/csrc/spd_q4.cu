@@ -18,7 +18,7 @@
 // off; both are exact for zeros up to 240.  Columns beyond `cols` and rows beyond `rows` hold code = zero and scale 0.
 //
 // Measured (graph of calls on different weights, against the bytes at the copy bandwidth): 151936 x 2560, one fp32 vector
-// 47 us for 201 MB (63 %); 2 x 12288 x 4096, 8 bf16 vectors, groups of 64 with zeros 18 us for 56 MB (45 %); Q, K and V of
+// 46 us for 201 MB (64 %); 2 x 12288 x 4096, 8 bf16 vectors, groups of 64 with zeros 18 us for 56 MB (45 %); Q, K and V of
 // 6144 x 4096 for one vector 8.5 us for 13 MB, of which some 6 us are launch, splitting the vector and joining; 4096 x 12288,
 // 16 vectors: bf16 16 us, fp32 30.
 #include <atomic>
@@ -523,14 +523,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const __grid_constant
       }
       if (r0 == r1) flush();  // an empty run between two others of a tile
       __syncthreads();
-      // Warps take tiles, or shares of a tile's vectors where there are fewer tiles; half a warp the 16 rows for a vector.  The
-      // parts of a tile are those of the warps whose runs touch it; the small terms are added first.
+      // Warps take tiles, or shares of a tile's vectors where there are fewer tiles; half a warp the 16 rows for a vector, and of a
+      // single vector the halves take a tile each.  The parts of a tile are those of the warps whose runs touch it; the small terms
+      // are added first.
       const bool done = kb_lo + nk == kb1;
-      const int nt = t1 - t0, ws = nt < kWarps ? kWarps / nt : 1;
-      for (int tl = nt < kWarps ? warp % nt : warp; tl < nt && warp < (nt < kWarps ? ws * nt : kWarps); tl += kWarps) {
+      const int nt = t1 - t0, two = mb == 1, crews = two ? 2 * kWarps : kWarps, crew = two ? 2 * warp + (lane >> 4) : warp;
+      const int ws = nt < crews ? crews / nt : 1, mc = nt < crews ? crew / nt : 0, m_first = two ? mc : 2 * mc + (lane >> 4);
+      for (int tl = nt < crews ? crew % nt : crew; tl < nt && mc < ws; tl += crews) {
         const int wa = ((tl * nk + 1) * kWarps - 1) / nrec, np = ((tl + 1) * nk * kWarps - 1) / nrec - wa + 1;
         const int r = tl * 16 + (lane & 15), row = (t0 - G.tile0) * 16 + r;
-        for (int m = (nt < kWarps ? warp / nt : 0) * 2 + (lane >> 4); m < mb; m += 2 * ws) {
+        for (int m = m_first; m < mb; m += two ? ws : 2 * ws) {
           const float* q = part + ((wa + tl) * 16 + (r & 15)) * PC + m * p.terms;
           const int o = m * nrow + r;
           float y = kb_lo > kb0 ? sums[o] : 0.f;

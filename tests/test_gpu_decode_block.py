@@ -707,3 +707,16 @@ assert not y.any() and (o - 1).abs().max() < 1e-5 and (small - 1).abs().max() < 
 """
     p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert p.returncode == 0, p.stderr[-2000:]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,P,cap,hq,hkv,hd", [
+    (1, 9000, 40, 8, 1, 128),     # one sequence and a long prefix: few runs of several chunks
+    (2, 8193, 300, 14, 2, 64),    # the last chunk holds one key
+    (330, 600, 5, 64, 16, 64),    # more tiles than SMs: runs that cross from tile to tile
+    (150, 5000, 3, 64, 8, 64),    # one tile an SM would leave half of them idle: runs that cross
+    (64, 4096, 20, 32, 8, 128),   # runs that end with their tiles
+])
+def test_shared_prefix_attention_runs(spd, dtype, B, P, cap, hq, hkv, hd):
+    assert spd.shared_prefix_attention_workspace_bytes(B, hq, hkv, hd, P) > 16
+    _check_attn(spd, B, P, cap, hq, hkv, hd, dtype)
