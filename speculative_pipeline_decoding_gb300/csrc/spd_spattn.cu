@@ -15,7 +15,7 @@
 // runs.  fp32 queries: one tile, Q and P as three bf16 terms (x = t0 + t1 + t2 to 24 bits), small terms first.  bf16
 // queries' probabilities are rounded to bf16 once, which adds to the output what its own rounding does (2^-9 of the rms).
 // The work, (row tiles) x (chunks), is cut into runs, one per SM, that end with their tiles where that leaves few SMs idle; a
-// run that crosses from one tile to the next leaves a part for each.  A chunk (64 KB at hd 128) is 2 x 2.1 M MACs a tile, 1024 cycles of tensor core, and 2790 cycles of an
+// run that crosses from one tile to the next leaves a part for each.  fp32 queries: runs of three chunks at most, for accuracy.  A chunk (64 KB at hd 128) is 2 x 2.1 M MACs a tile, 1024 cycles of tensor core, and 2790 cycles of an
 // SM's share of the memory: that bounds up to about 256 rows a kv head, softmax and tensor core beyond (measured a chunk of
 // two tiles: 850 cycles of exponentials, 400 of maxima, 2 x 1024 of MMAs).  Alone, 64 x 4 rows a kv head x 32768 keys take
 // 30 us (134 MB: 4.5 TB/s, 1.1 PFLOP/s).
@@ -1111,6 +1111,13 @@ void prefix_geometry(int rows, int hkv, int P, int ns, int sms, Params* p) {
   } else {
     p->n_cta = (int)(total < sms ? total : sms);
   }
+  // fp32 queries: runs of 3 chunks at most, over more blocks than SMs if need be.  The tensor core truncates its sums, and what
+  // a sum loses grows with its steps: 5e-7 of the result after one chunk, 8e-7 after two, 1.7e-6 after four, where fp32
+  // products rounded to nearest are 1e-6 off.  (Up to 1024 runs of a unit: beyond 393216 keys the runs grow.)
+  if (ns == 1) {
+    const int runs = (p->nch + 2) / 3 < 1024 ? (p->nch + 2) / 3 : 1024;
+    if ((long long)p->n_cta < (long long)p->units * runs) p->n_cta = p->units * runs;
+  }
 }
 size_t part_rows(const Params& p, int ns) { return ((size_t)p.n_cta + p.units) * ns * kTile; }
 // Runs of a sequence's own keys: 4096 in all where the batch is smaller, 16 of a sequence at most.
@@ -1204,7 +1211,7 @@ cudaError_t launch(Params& p, void* workspace, cudaStream_t s) {
   p.own_run = p.max_seq > 0 ? (int)((p.max_seq + most - 1) / most + 15) / 16 * 16 : 16;
   if (p.own_run < 128) p.own_run = 128;
   p.own_runs = p.max_seq > 0 ? (int)((p.max_seq + p.own_run - 1) / p.own_run) : 1;
-  p.parts = p.own_runs + p.n_cta;
+  p.parts = p.own_runs + (p.n_cta + p.units - 1) / p.units + 2;  // of a row, at most
   PrefixMaps maps;
   e = encode_map(&maps.k, p.pk, HD, p.P, p.prefix_cap, p.hkv, kTile);
   if (e == cudaSuccess) e = encode_map(&maps.v, p.pv, HD, p.P, p.prefix_cap, p.hkv, kTile);
